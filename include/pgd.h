@@ -275,6 +275,159 @@ pgd_status pgd_paged_decode_attention_ex(
     void *workspace, size_t workspace_bytes, int32_t num_ctas, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* Prompt attention                                                         */
+/* ------------------------------------------------------------------------ */
+/*
+ * pgd_prefill_attention -- causal attention of whole prompts, packed one
+ * after another: the stage before decode, where every token of a prompt is a
+ * query ("attention kernels", sections "standard attention", "FlashAttention"
+ * and "prefill and decode attention").
+ *
+ * Sequence s holds the packed rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1, its
+ * positions 0 .. n - 1.  For its row i and query head a (KV head a / g):
+ *   x_t = scale * sum_d q[i][a][d] * k[t][a / g][d]
+ *   out = sum_t exp(x_t - M) v[t][a / g] / sum_t exp(x_t - M),  M = max_t x_t
+ *   lse = M + ln sum_t exp(x_t - M)
+ * over the visible positions t: t <= i, and with window > 0 also
+ * t > i - window.  A key that a row does not see has no influence on it, not
+ * even if it holds infinities or NaN.
+ *
+ *   q            device bf16, row i at q + i * q_stride: [num_q_heads][head_dim]
+ *   k, v         device bf16, row i at k + i * k_stride (v + i * v_stride):
+ *                [num_kv_heads][head_dim]; all three 16-byte aligned.  The
+ *                strides are in elements, at least a row's width and
+ *                multiples of 8, so the three may be slices of one fused
+ *                projection
+ *   cu_seqlens   device int32 [num_seqs + 1], not decreasing, each in
+ *                [0, num_tokens]; a sequence that breaks this flags
+ *                PGD_ERR_DEVICE_BOUNDS and is skipped
+ *   num_tokens   rows that q, k, v, out and lse_out hold; rows that belong to
+ *                no sequence are neither read nor written
+ *   max_seq_len  host hint >= every length (0 = unknown); only used to choose
+ *                the number of splits
+ *   window       0 = the whole causal range; > 0 = the last `window` positions
+ *   num_q_heads % num_kv_heads == 0, g = num_q_heads / num_kv_heads in
+ *                1 .. 16; head_dim in {128, 256}
+ *   out          device bf16 [num_tokens][num_q_heads][head_dim], 16-byte
+ *                aligned (rounded once, from fp32)
+ *   lse_out      optional device fp32 [num_tokens][num_q_heads] (natural log)
+ *   workspace, workspace_bytes, num_splits   few query rows over many keys
+ *                leave SMs idle; the keys are then cut into splits whose
+ *                unrounded results go to the workspace and are merged by
+ *                log-sum-exp in a second kernel.  num_splits = 0 lets the
+ *                library choose, 1 .. 64 forces a count.  The workspace (any
+ *                contents, 16-byte aligned, this call's alone until it has
+ *                run) holds pgd_prefill_workspace_bytes(...) bytes; with
+ *                num_splits = 0 and a smaller one or NULL the call runs with
+ *                the splits that fit, with a forced count it returns
+ *                PGD_ERR_WORKSPACE
+ *   stream       cudaStream_t as void*
+ * Weights enter the second product as bf16 (half a step: 2^-8 of each weight)
+ * and the normaliser sums them in fp32 before that rounding.  Repeated calls
+ * with the same inputs and split count give the same bits.  num_seqs = 0 or
+ * num_tokens = 0 enqueues nothing.
+ */
+pgd_status pgd_prefill_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                 const void *v, int64_t v_stride, const int32_t *cu_seqlens,
+                                 int32_t num_seqs, int32_t num_tokens, int32_t max_seq_len,
+                                 int32_t window, int32_t num_q_heads, int32_t num_kv_heads,
+                                 int32_t head_dim, float scale, void *out, float *lse_out,
+                                 void *workspace, size_t workspace_bytes, int32_t num_splits,
+                                 void *stream);
+
+/*
+ * pgd_paged_prefill_attention -- the same for the newest tokens of sequences
+ * whose K/V, those tokens' included, is in the paged cache: a chunk of a
+ * prompt behind its prefix, a prompt behind a shared prefix, draft tokens to
+ * verify, or single tokens, each sequence with its own count ("attention
+ * kernels", section "paged KV and kernels"; chunked prefill of the inference
+ * lecture).  pgd_kv_append of the new rows comes first.
+ *
+ * Sequence s has n = context_lens[s] cached positions; its
+ * L = cu_seqlens[s + 1] - cu_seqlens[s] query rows are the positions
+ * n - L .. n - 1, and each sees the positions up to its own (with window > 0
+ * the last `window` of them).  A row at a negative position (n < L) sees
+ * nothing: out = 0, lse = -inf.  FP8 E4M3 caches as in
+ * pgd_paged_decode_attention.
+ *
+ *   q, q_stride, cu_seqlens, num_tokens, window, out, lse_out, workspace,
+ *   num_splits   as pgd_prefill_attention
+ *   k_cache, v_cache, block_table, max_blocks_per_seq, context_lens,
+ *   block_size, num_blocks, kv_dtype, k_scale, v_scale   as
+ *                pgd_paged_decode_attention; blocks that no row of a sequence
+ *                sees are not read.  head_dim 256 with bf16 only
+ *   max_q_len, max_context_len  host hints >= every L and n (0 = unknown);
+ *                only used to choose the number of splits
+ * With an FP8 cache the weights enter the second product as f16 (half a step:
+ * 2^-11).
+ */
+pgd_status pgd_paged_prefill_attention(
+    const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+    const int32_t *block_table, int32_t max_blocks_per_seq, const int32_t *context_lens,
+    const int32_t *cu_seqlens, int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
+    int32_t max_context_len, int32_t window, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale, pgd_kv_dtype kv_dtype,
+    const float *k_scale, const float *v_scale, void *out, float *lse_out, void *workspace,
+    size_t workspace_bytes, int32_t num_splits, void *stream);
+
+/*
+ * pgd_prefill_workspace_bytes -- bytes of workspace that the two calls above
+ * use on the current device for these sizes (max_context_len: the hint of
+ * max_seq_len for the packed form; 0 for a hint = unknown).  0 means that the
+ * call does not split, or invalid sizes.
+ */
+size_t pgd_prefill_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
+                                   int32_t max_context_len, int32_t num_q_heads,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t num_splits);
+
+/* ------------------------------------------------------------------------ */
+/* An FP8 cache's scales, and rows of a cache read back                     */
+/* ------------------------------------------------------------------------ */
+/*
+ * pgd_kv_quant_scales -- the per-KV-head scales that pgd_kv_append_quant and
+ * the FP8 attention calls take, from K/V rows (of a prompt, or of calibration
+ * batches): for K and for V,
+ *   scale[h] = max(max over t, d of |x[t][h][d]| / 448, 2^-40)
+ * so that the largest element lands on E4M3's largest value.  The maximum is
+ * over finite elements (pgd_kv_append_quant saturates infinities); the
+ * quotient is the fp32 one; the floor keeps a head of zeros divisible.
+ *
+ *   k_new, v_new  device bf16 [num_tokens][num_kv_heads][head_dim], 16-byte
+ *                 aligned
+ *   accumulate    0: the scales are written; 1: they are raised where these
+ *                 rows need it (the first call of a calibration passes 0)
+ *   k_scale, v_scale  device fp32 [num_kv_heads]
+ *   num_tokens >= 0 (0 with accumulate = 0 writes the floor); head_dim in
+ *   {128, 256}; num_kv_heads in 1 .. 65536.
+ * Bit-exact with that definition.
+ */
+pgd_status pgd_kv_quant_scales(const void *k_new, const void *v_new, int32_t num_tokens,
+                               int32_t num_kv_heads, int32_t head_dim, int32_t accumulate,
+                               float *k_scale, float *v_scale, void *stream);
+
+/*
+ * pgd_kv_gather -- the inverse of the appends: row t of k_out and v_out is the
+ * cached row of slot slot_mapping[t] (physical block slot / block_size, row
+ * slot % block_size), as bf16.  bf16 rows are copied bit for bit; E4M3 rows
+ * are the fp32 product e4m3 * scale[h] rounded to nearest even.
+ *
+ *   k_cache, v_cache  device, HND layout, 16-byte aligned
+ *   slot_mapping   device int64 [num_tokens]; a slot < 0 leaves its output row
+ *                  as it was; a slot >= num_blocks * block_size does too and
+ *                  flags PGD_ERR_DEVICE_BOUNDS.  Slots may repeat
+ *   k_out, v_out   device bf16 [num_tokens][num_kv_heads][head_dim], 16-byte
+ *                  aligned, apart from the caches
+ *   k_scale, v_scale  device fp32 [num_kv_heads] for FP8 (NULL for bf16)
+ *   num_tokens >= 0 (0 enqueues nothing); head_dim in {128, 256}; block_size
+ *   in {16, 32, 64}; num_kv_heads in 1 .. 65536.
+ */
+pgd_status pgd_kv_gather(const void *k_cache, const void *v_cache, const int64_t *slot_mapping,
+                         int32_t num_tokens, void *k_out, void *v_out, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                         pgd_kv_dtype kv_dtype, const float *k_scale, const float *v_scale,
+                         void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* Consumer math of the decode kernels                                      */
 /* ------------------------------------------------------------------------ */
 /*

@@ -1,4 +1,4 @@
-"""Paged GQA decode attention for B200 (sm_100a).
+"""Paged GQA attention for B200 (sm_100a): prompts, then decode.
 
 The compute lives in libpgd.so (hand-written CUDA, C ABI in include/pgd.h);
 this package only marshals torch tensors to it.  `kvp` splits one sequence's
@@ -10,6 +10,8 @@ from ._binding import (  # noqa: F401
     paged_decode_attention_noalloc, paged_decode_partial, kvp_plan, decode_step,
     merge_partials, decode_workspace_bytes, get_device_error, shutdown, set_decode_math,
     get_decode_math, debug_set_wait_limit_ns, debug_get_wait_limit_ns, decode_grid,
+    prefill_attention, paged_prefill_attention, prefill_workspace_bytes, kv_quant_scales,
+    kv_gather,
 )
 from . import kvp  # noqa: F401,E402
 
@@ -18,4 +20,5 @@ __all__ = ["kv_append", "kv_append_quant", "paged_decode_attention", "paged_deco
            "merge_partials", "decode_workspace_bytes", "get_device_error", "shutdown",
            "set_decode_math", "get_decode_math", "debug_set_wait_limit_ns",
            "debug_get_wait_limit_ns", "decode_grid", "PGDError", "load_library", "lib_path", "kvp",
-           "PGD_KV_BF16", "PGD_KV_FP8_E4M3"]
+           "prefill_attention", "paged_prefill_attention", "prefill_workspace_bytes",
+           "kv_quant_scales", "kv_gather", "PGD_KV_BF16", "PGD_KV_FP8_E4M3"]

@@ -92,6 +92,19 @@ def load_library():
                                                        i32, i32, i32, f32, st, P, P, P, P, i32, P]
     lib.pgd_merge_partials.restype = st
     lib.pgd_merge_partials.argtypes = [P, P, i32, i32, i32, P, P, P]
+    lib.pgd_prefill_attention.restype = st
+    lib.pgd_prefill_attention.argtypes = [P, i64, P, i64, P, i64, P, i32, i32, i32, i32, i32, i32,
+                                          i32, f32, P, P, P, sz, i32, P]
+    lib.pgd_paged_prefill_attention.restype = st
+    lib.pgd_paged_prefill_attention.argtypes = [P, i64, P, P, P, i32, P, P, i32, i32, i32, i32,
+                                                i32, i32, i32, i32, i32, i32, f32, st, P, P, P, P,
+                                                P, sz, i32, P]
+    lib.pgd_prefill_workspace_bytes.restype = sz
+    lib.pgd_prefill_workspace_bytes.argtypes = [i32] * 8
+    lib.pgd_kv_quant_scales.restype = st
+    lib.pgd_kv_quant_scales.argtypes = [P, P, i32, i32, i32, i32, P, P, P]
+    lib.pgd_kv_gather.restype = st
+    lib.pgd_kv_gather.argtypes = [P, P, P, i32, P, P, i32, i32, i32, i32, st, P, P, P]
     lib.pgd_get_device_error.restype = st
     lib.pgd_get_device_error.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
     lib.pgd_shutdown.restype = st
@@ -101,7 +114,6 @@ def load_library():
     lib.paged_decode_attention.restype = st
     lib.paged_decode_attention.argtypes = [P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32,
                                            f32, P, P]
-    del i64
     _lib = lib
     return lib
 
@@ -122,9 +134,10 @@ class Prepared:
     it was prepared with and returns what the original call returned.  The
     tensors must stay alive and keep their storage while it is in use."""
 
-    __slots__ = ("_fn", "_args", "_name", "result")
+    __slots__ = ("_fn", "_args", "_name", "result", "_keep")
 
-    def __init__(self, fn, args, name, result):
+    def __init__(self, fn, args, name, result, keep=None):
+        self._keep = keep            # a workspace that the binding allocated
         conv = []
         for t, a in zip(fn.argtypes, args):
             conv.append(a if a is None or isinstance(a, t) else t(a))
@@ -137,10 +150,10 @@ class Prepared:
         return self.result
 
 
-def _issue(fn, name: str, args, prepare: bool, result=None):
+def _issue(fn, name: str, args, prepare: bool, result=None, keep=None):
     """Run the C call now, or return it prepared (see Prepared)."""
     if prepare:
-        return Prepared(fn, args, name, result)
+        return Prepared(fn, args, name, result, keep)
     _check(fn(*args), name)
     return result
 
@@ -519,6 +532,218 @@ def merge_partials(o_part, lse_part, out=None, lse_out=None, *, stream=None, pre
     return _issue(lib.pgd_merge_partials, "pgd_merge_partials",
                   (_ptr(o_part), _ptr(lse_part), P, R, D, _ptr(out), _ptr(lse_out),
                    _stream(stream)), prepare, out)
+
+
+def _same_device(where: str, *tensors):
+    """The library works on the current CUDA device; tensors of another one
+    would be read there as foreign pointers."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"{where}: a tensor is on {t.device}, the current device is "
+                             f"cuda:{cur}")
+
+
+def _rows(t, name: str, heads: int, dim: int) -> int:
+    """Check packed rows [T][heads][dim] whose tokens may be strided (a slice
+    of a fused projection); returns the token stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.bfloat16")
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
+        raise ValueError(f"{name} must be [tokens][{heads}][{dim}], got {tuple(t.shape)}")
+    if t.shape[0] == 0:
+        return heads * dim
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _prefill_workspace(workspace, need: int, device, stream):
+    """(workspace, bytes): the caller's, or one from torch's allocator on the
+    launching stream when the call can use one."""
+    if workspace is not None:
+        _need(workspace, "workspace", None)
+        return workspace, workspace.numel() * workspace.element_size()
+    if need == 0:
+        return None, 0
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    if isinstance(stream, torch.cuda.Stream):
+        ws.record_stream(stream)
+    elif stream is not None:
+        ws.record_stream(torch.cuda.ExternalStream(int(stream)))
+    return ws, need
+
+
+def prefill_workspace_bytes(num_seqs: int, num_tokens: int, max_q_len: int, max_context_len: int,
+                            num_q_heads: int, num_kv_heads: int, head_dim: int,
+                            num_splits: int = 0) -> int:
+    """Workspace of the prompt attention calls (pgd_prefill_workspace_bytes)."""
+    return int(load_library().pgd_prefill_workspace_bytes(
+        int(num_seqs), int(num_tokens), int(max_q_len), int(max_context_len), int(num_q_heads),
+        int(num_kv_heads), int(head_dim), int(num_splits)))
+
+
+def prefill_attention(q, k, v, cu_seqlens, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                      scale: float, out: Optional[torch.Tensor] = None, *, window: int = 0,
+                      max_seq_len: int = 0, lse_out=None, workspace=None, num_splits: int = 0,
+                      stream=None, prepare=False):
+    """Causal attention of packed prompts (pgd_prefill_attention).
+
+    q bf16 [T][Hq][D], k / v bf16 [T][Hkv][D]; the token stride is free (a
+    multiple of 8 elements), so slices of one fused projection are taken as
+    they are.  cu_seqlens int32 [B + 1]: sequence s holds rows cu[s] to
+    cu[s + 1] - 1.  window > 0 keeps the last `window` positions.  Returns out
+    (bf16 [T][Hq][D]); lse_out (fp32 [T][Hq]) is filled when given.  Rows of
+    no sequence are left as they were.  workspace: None lets the binding
+    allocate what the splits need.
+    """
+    lib = load_library()
+    qs = _rows(q, "q", num_q_heads, head_dim)
+    ks = _rows(k, "k", num_kv_heads, head_dim)
+    vs = _rows(v, "v", num_kv_heads, head_dim)
+    _need(cu_seqlens, "cu_seqlens", (torch.int32,), 1)
+    T, B = q.shape[0], cu_seqlens.shape[0] - 1
+    if k.shape[0] != T or v.shape[0] != T or B < 0:
+        raise ValueError("prefill_attention: inconsistent shapes")
+    if out is None:
+        out = torch.empty((T, num_q_heads, head_dim), dtype=torch.bfloat16, device=q.device)
+    _need(out, "out", (torch.bfloat16,), 3)
+    if lse_out is not None:
+        _need(lse_out, "lse_out", (torch.float32,), 2)
+    if tuple(out.shape) != (T, num_q_heads, head_dim) or (
+            lse_out is not None and tuple(lse_out.shape) != (T, num_q_heads)):
+        raise ValueError("prefill_attention: output shapes")
+    _same_device("prefill_attention", q, k, v, cu_seqlens, out, lse_out, workspace)
+    need = prefill_workspace_bytes(B, T, max_seq_len, max_seq_len, num_q_heads, num_kv_heads,
+                                   head_dim, num_splits) if workspace is None else 0
+    ws, ws_bytes = _prefill_workspace(workspace, need, q.device, stream)
+    return _issue(lib.pgd_prefill_attention, "pgd_prefill_attention", (
+        _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(cu_seqlens), B, T, int(max_seq_len),
+        int(window), num_q_heads, num_kv_heads, head_dim, float(scale), _ptr(out), _ptr(lse_out),
+        _ptr(ws), ws_bytes, int(num_splits), _stream(stream)), prepare, out, ws)
+
+
+def paged_prefill_attention(q, k_cache, v_cache, block_table, context_lens, cu_seqlens,
+                            num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
+                            scale: float, out: Optional[torch.Tensor] = None, *, window: int = 0,
+                            max_q_len: int = 0, max_context_len: int = 0, k_scale=None,
+                            v_scale=None, lse_out=None, workspace=None, num_splits: int = 0,
+                            stream=None, prepare=False):
+    """Causal attention of each sequence's newest tokens over the paged cache
+    that already holds them (pgd_paged_prefill_attention).
+
+    q bf16 [T][Hq][D] (free token stride): sequence s's queries are rows
+    cu_seqlens[s] to cu_seqlens[s + 1] - 1, its newest tokens, counted in
+    context_lens[s].  Caches, block_table, scales as paged_decode_attention;
+    window, out, lse_out, workspace as prefill_attention.
+    """
+    lib = load_library()
+    qs = _rows(q, "q", num_q_heads, head_dim)
+    _need(k_cache, "k_cache", _KV_DTYPES, 4)
+    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
+    _need(block_table, "block_table", (torch.int32,), 2)
+    _need(context_lens, "context_lens", (torch.int32,), 1)
+    _need(cu_seqlens, "cu_seqlens", (torch.int32,), 1)
+    T, B = q.shape[0], context_lens.shape[0]
+    if tuple(k_cache.shape[1:]) != (num_kv_heads, block_size, head_dim) or \
+            v_cache.shape != k_cache.shape or block_table.shape[0] != B or \
+            cu_seqlens.shape[0] != B + 1:
+        raise ValueError("paged_prefill_attention: inconsistent shapes")
+    kvd = _kv_dtype(k_cache)
+    if kvd == PGD_KV_FP8_E4M3:
+        _need(k_scale, "k_scale", (torch.float32,), 1)
+        _need(v_scale, "v_scale", (torch.float32,), 1)
+        if k_scale.shape != (num_kv_heads,) or v_scale.shape != (num_kv_heads,):
+            raise ValueError("paged_prefill_attention: scale shapes")
+    else:
+        k_scale = v_scale = None
+    if out is None:
+        out = torch.empty((T, num_q_heads, head_dim), dtype=torch.bfloat16, device=q.device)
+    _need(out, "out", (torch.bfloat16,), 3)
+    if lse_out is not None:
+        _need(lse_out, "lse_out", (torch.float32,), 2)
+    if tuple(out.shape) != (T, num_q_heads, head_dim) or (
+            lse_out is not None and tuple(lse_out.shape) != (T, num_q_heads)):
+        raise ValueError("paged_prefill_attention: output shapes")
+    _same_device("paged_prefill_attention", q, k_cache, v_cache, block_table, context_lens,
+                 cu_seqlens, k_scale, v_scale, out, lse_out, workspace)
+    cap = block_table.shape[1] * block_size
+    need = prefill_workspace_bytes(B, T, max_q_len, int(max_context_len) or cap, num_q_heads,
+                                   num_kv_heads, head_dim, num_splits) if workspace is None else 0
+    ws, ws_bytes = _prefill_workspace(workspace, need, q.device, stream)
+    return _issue(lib.pgd_paged_prefill_attention, "pgd_paged_prefill_attention", (
+        _ptr(q), qs, _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
+        _ptr(context_lens), _ptr(cu_seqlens), B, T, int(max_q_len), int(max_context_len),
+        int(window), num_q_heads, num_kv_heads, head_dim, block_size, k_cache.shape[0],
+        float(scale), kvd, _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse_out), _ptr(ws),
+        ws_bytes, int(num_splits), _stream(stream)), prepare, out, ws)
+
+
+def kv_quant_scales(k_new, v_new, k_scale: Optional[torch.Tensor] = None,
+                    v_scale: Optional[torch.Tensor] = None, *, accumulate: bool = False,
+                    stream=None, prepare=False):
+    """Per-KV-head FP8 scales from bf16 rows [N][Hkv][D] (pgd_kv_quant_scales):
+    amax / 448, at least 2^-40.  accumulate=True raises the given scales
+    where these rows need it.  Returns (k_scale, v_scale), fp32 [Hkv]."""
+    lib = load_library()
+    _need(k_new, "k_new", (torch.bfloat16,), 3)
+    _need(v_new, "v_new", (torch.bfloat16,), 3)
+    n, hkv, d = k_new.shape
+    if accumulate and (k_scale is None or v_scale is None):
+        raise ValueError("kv_quant_scales: accumulate needs k_scale and v_scale")
+    if k_scale is None:
+        k_scale = torch.empty(hkv, dtype=torch.float32, device=k_new.device)
+    if v_scale is None:
+        v_scale = torch.empty(hkv, dtype=torch.float32, device=k_new.device)
+    _need(k_scale, "k_scale", (torch.float32,), 1)
+    _need(v_scale, "v_scale", (torch.float32,), 1)
+    if v_new.shape != k_new.shape or k_scale.shape != (hkv,) or v_scale.shape != (hkv,):
+        raise ValueError("kv_quant_scales: inconsistent shapes")
+    _same_device("kv_quant_scales", k_new, v_new, k_scale, v_scale)
+    return _issue(lib.pgd_kv_quant_scales, "pgd_kv_quant_scales",
+                  (_ptr(k_new), _ptr(v_new), n, hkv, d, 1 if accumulate else 0, _ptr(k_scale),
+                   _ptr(v_scale), _stream(stream)), prepare, (k_scale, v_scale))
+
+
+def kv_gather(k_cache, v_cache, slot_mapping, k_out: Optional[torch.Tensor] = None,
+              v_out: Optional[torch.Tensor] = None, *, k_scale=None, v_scale=None, stream=None,
+              prepare=False):
+    """Cached rows read back as bf16 (pgd_kv_gather): row t of the outputs
+    [N][Hkv][D] is the row of slot slot_mapping[t]; FP8 rows are multiplied by
+    their head's scale.  Rows of negative slots are left as they were.
+    Returns (k_out, v_out)."""
+    lib = load_library()
+    _need(k_cache, "k_cache", _KV_DTYPES, 4)
+    _need(v_cache, "v_cache", (k_cache.dtype,), 4)
+    _need(slot_mapping, "slot_mapping", (torch.int64,), 1)
+    nb, hkv, bs, d = k_cache.shape
+    n = slot_mapping.shape[0]
+    kvd = _kv_dtype(k_cache)
+    if kvd == PGD_KV_FP8_E4M3:
+        _need(k_scale, "k_scale", (torch.float32,), 1)
+        _need(v_scale, "v_scale", (torch.float32,), 1)
+        if k_scale.shape != (hkv,) or v_scale.shape != (hkv,):
+            raise ValueError("kv_gather: scale shapes")
+    else:
+        k_scale = v_scale = None
+    if k_out is None:
+        k_out = torch.empty((n, hkv, d), dtype=torch.bfloat16, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty((n, hkv, d), dtype=torch.bfloat16, device=k_cache.device)
+    _need(k_out, "k_out", (torch.bfloat16,), 3)
+    _need(v_out, "v_out", (torch.bfloat16,), 3)
+    if v_cache.shape != k_cache.shape or tuple(k_out.shape) != (n, hkv, d) or \
+            v_out.shape != k_out.shape:
+        raise ValueError("kv_gather: inconsistent shapes")
+    _same_device("kv_gather", k_cache, v_cache, slot_mapping, k_out, v_out, k_scale, v_scale)
+    return _issue(lib.pgd_kv_gather, "pgd_kv_gather",
+                  (_ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), n, _ptr(k_out), _ptr(v_out),
+                   hkv, d, bs, nb, kvd, _ptr(k_scale), _ptr(v_scale), _stream(stream)), prepare,
+                  (k_out, v_out))
 
 
 def get_device_error(*, stream=None) -> int:

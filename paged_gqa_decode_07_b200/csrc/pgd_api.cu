@@ -14,6 +14,7 @@
 
 #include "pgd.h"
 #include "pgd_grid.h"
+#include "pgd_host.h"
 #include "pgd_launch.h"
 
 namespace {
@@ -235,6 +236,42 @@ bool supported_block(int bs) { return bs == 16 || bs == 32 || bs == 64; }
 bool supported_group(int g) { return g >= 1 && g <= 16; }
 
 }  // namespace
+
+namespace pgd {
+
+pgd_status device_info(int *sms, uint32_t **flags) {
+    DeviceState *d = nullptr;
+    const pgd_status st = device_state(&d);
+    if (st != PGD_OK) return st;
+    *sms = d->sms;
+    *flags = d->flags;
+    return PGD_OK;
+}
+
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+
+pgd_status encode_tiled_map(CUtensorMap *m, const void *base, int elem_bytes, int rank,
+                            const uint64_t *dims, const uint64_t *strides, const uint32_t *box) {
+    auto fn = encode_fn();
+    if (!fn) return PGD_ERR_CUDA;
+    cuuint64_t d[5], s[5];
+    cuuint32_t b[5], e[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        e[i] = 1;
+        if (i + 1 < rank) s[i] = strides[i];
+    }
+    const CUresult r = fn(m,
+                          elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                          static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, s, b, e,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PGD_OK : PGD_ERR_CUDA;
+}
+
+}  // namespace pgd
 
 extern "C" {
 
