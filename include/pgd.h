@@ -304,27 +304,26 @@ pgd_status pgd_paged_decode_attention_ex(
  *   num_tokens   rows that q, k, v, out and lse_out hold; rows that belong to
  *                no sequence are neither read nor written
  *   max_seq_len  host hint >= every length (0 = unknown); only used to choose
- *                the number of splits
+ *                whether work is cut
  *   window       0 = the whole causal range; > 0 = the last `window` positions
  *   num_q_heads % num_kv_heads == 0, g = num_q_heads / num_kv_heads in
  *                1 .. 16; head_dim in {128, 256}
  *   out          device bf16 [num_tokens][num_q_heads][head_dim], 16-byte
  *                aligned (rounded once, from fp32)
  *   lse_out      optional device fp32 [num_tokens][num_q_heads] (natural log)
- *   workspace, workspace_bytes, num_splits   few query rows over many keys
- *                leave SMs idle; the keys are then cut into splits whose
- *                unrounded results go to the workspace and are merged by
- *                log-sum-exp in a second kernel.  num_splits = 0 lets the
- *                library choose, 1 .. 64 forces a count.  The workspace (any
- *                contents, 16-byte aligned, this call's alone until it has
- *                run) holds pgd_prefill_workspace_bytes(...) bytes; with
- *                num_splits = 0 and a smaller one or NULL the call runs with
- *                the splits that fit, with a forced count it returns
- *                PGD_ERR_WORKSPACE
+ *   workspace, workspace_bytes, num_ctas   the work (query rows times keys) is
+ *                dealt in equal shares to num_ctas CTAs; 0 = automatic, 1 ..
+ *                1024 forces a number.  The query rows whose keys a boundary
+ *                cuts leave unrounded results in the workspace, which a second
+ *                kernel merges by log-sum-exp.  The workspace (any contents,
+ *                16-byte aligned, this call's alone until it has run) holds
+ *                pgd_prefill_workspace_bytes(...) bytes; with num_ctas = 0 and
+ *                a smaller one or NULL nothing is cut, with num_ctas > 1 the
+ *                call returns PGD_ERR_WORKSPACE
  *   stream       cudaStream_t as void*
  * Weights enter the second product as bf16 (half a step: 2^-8 of each weight)
  * and the normaliser sums them in fp32 before that rounding.  Repeated calls
- * with the same inputs and split count give the same bits.  num_seqs = 0 or
+ * with the same inputs and num_ctas give the same bits.  num_seqs = 0 or
  * num_tokens = 0 enqueues nothing.
  */
 pgd_status pgd_prefill_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
@@ -332,7 +331,7 @@ pgd_status pgd_prefill_attention(const void *q, int64_t q_stride, const void *k,
                                  int32_t num_seqs, int32_t num_tokens, int32_t max_seq_len,
                                  int32_t window, int32_t num_q_heads, int32_t num_kv_heads,
                                  int32_t head_dim, float scale, void *out, float *lse_out,
-                                 void *workspace, size_t workspace_bytes, int32_t num_splits,
+                                 void *workspace, size_t workspace_bytes, int32_t num_ctas,
                                  void *stream);
 
 /*
@@ -351,13 +350,13 @@ pgd_status pgd_prefill_attention(const void *q, int64_t q_stride, const void *k,
  * pgd_paged_decode_attention.
  *
  *   q, q_stride, cu_seqlens, num_tokens, window, out, lse_out, workspace,
- *   num_splits   as pgd_prefill_attention
+ *   num_ctas     as pgd_prefill_attention
  *   k_cache, v_cache, block_table, max_blocks_per_seq, context_lens,
  *   block_size, num_blocks, kv_dtype, k_scale, v_scale   as
  *                pgd_paged_decode_attention; blocks that no row of a sequence
  *                sees are not read.  head_dim 256 with bf16 only
  *   max_q_len, max_context_len  host hints >= every L and n (0 = unknown);
- *                only used to choose the number of splits
+ *                only used to choose whether work is cut
  * With an FP8 cache the weights enter the second product as f16 (half a step:
  * 2^-11).
  */
@@ -368,17 +367,17 @@ pgd_status pgd_paged_prefill_attention(
     int32_t max_context_len, int32_t window, int32_t num_q_heads, int32_t num_kv_heads,
     int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale, pgd_kv_dtype kv_dtype,
     const float *k_scale, const float *v_scale, void *out, float *lse_out, void *workspace,
-    size_t workspace_bytes, int32_t num_splits, void *stream);
+    size_t workspace_bytes, int32_t num_ctas, void *stream);
 
 /*
  * pgd_prefill_workspace_bytes -- bytes of workspace that the two calls above
- * use on the current device for these sizes (max_context_len: the hint of
- * max_seq_len for the packed form; 0 for a hint = unknown).  0 means that the
- * call does not split, or invalid sizes.
+ * use on the current device for these sizes (max_context_len: the hint, of
+ * max_seq_len for the packed form; 0 = unknown).  0 means that the call does
+ * not cut, or invalid sizes.
  */
-size_t pgd_prefill_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
-                                   int32_t max_context_len, int32_t num_q_heads,
-                                   int32_t num_kv_heads, int32_t head_dim, int32_t num_splits);
+size_t pgd_prefill_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t max_context_len,
+                                   int32_t window, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t num_ctas);
 
 /* ------------------------------------------------------------------------ */
 /* An FP8 cache's scales, and rows of a cache read back                     */

@@ -578,18 +578,18 @@ def _prefill_workspace(workspace, need: int, device, stream):
     return ws, need
 
 
-def prefill_workspace_bytes(num_seqs: int, num_tokens: int, max_q_len: int, max_context_len: int,
+def prefill_workspace_bytes(num_seqs: int, num_tokens: int, max_context_len: int, window: int,
                             num_q_heads: int, num_kv_heads: int, head_dim: int,
-                            num_splits: int = 0) -> int:
+                            num_ctas: int = 0) -> int:
     """Workspace of the prompt attention calls (pgd_prefill_workspace_bytes)."""
     return int(load_library().pgd_prefill_workspace_bytes(
-        int(num_seqs), int(num_tokens), int(max_q_len), int(max_context_len), int(num_q_heads),
-        int(num_kv_heads), int(head_dim), int(num_splits)))
+        int(num_seqs), int(num_tokens), int(max_context_len), int(window), int(num_q_heads),
+        int(num_kv_heads), int(head_dim), int(num_ctas)))
 
 
 def prefill_attention(q, k, v, cu_seqlens, num_q_heads: int, num_kv_heads: int, head_dim: int,
                       scale: float, out: Optional[torch.Tensor] = None, *, window: int = 0,
-                      max_seq_len: int = 0, lse_out=None, workspace=None, num_splits: int = 0,
+                      max_seq_len: int = 0, lse_out=None, workspace=None, num_ctas: int = 0,
                       stream=None, prepare=False):
     """Causal attention of packed prompts (pgd_prefill_attention).
 
@@ -599,7 +599,7 @@ def prefill_attention(q, k, v, cu_seqlens, num_q_heads: int, num_kv_heads: int, 
     cu[s + 1] - 1.  window > 0 keeps the last `window` positions.  Returns out
     (bf16 [T][Hq][D]); lse_out (fp32 [T][Hq]) is filled when given.  Rows of
     no sequence are left as they were.  workspace: None lets the binding
-    allocate what the splits need.
+    allocate what cut work needs.
     """
     lib = load_library()
     qs = _rows(q, "q", num_q_heads, head_dim)
@@ -618,20 +618,20 @@ def prefill_attention(q, k, v, cu_seqlens, num_q_heads: int, num_kv_heads: int, 
             lse_out is not None and tuple(lse_out.shape) != (T, num_q_heads)):
         raise ValueError("prefill_attention: output shapes")
     _same_device("prefill_attention", q, k, v, cu_seqlens, out, lse_out, workspace)
-    need = prefill_workspace_bytes(B, T, max_seq_len, max_seq_len, num_q_heads, num_kv_heads,
-                                   head_dim, num_splits) if workspace is None else 0
+    need = prefill_workspace_bytes(B, T, min(max_seq_len or T, T), window, num_q_heads,
+                                   num_kv_heads, head_dim, num_ctas) if workspace is None else 0
     ws, ws_bytes = _prefill_workspace(workspace, need, q.device, stream)
     return _issue(lib.pgd_prefill_attention, "pgd_prefill_attention", (
         _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(cu_seqlens), B, T, int(max_seq_len),
         int(window), num_q_heads, num_kv_heads, head_dim, float(scale), _ptr(out), _ptr(lse_out),
-        _ptr(ws), ws_bytes, int(num_splits), _stream(stream)), prepare, out, ws)
+        _ptr(ws), ws_bytes, int(num_ctas), _stream(stream)), prepare, out, ws)
 
 
 def paged_prefill_attention(q, k_cache, v_cache, block_table, context_lens, cu_seqlens,
                             num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
                             scale: float, out: Optional[torch.Tensor] = None, *, window: int = 0,
                             max_q_len: int = 0, max_context_len: int = 0, k_scale=None,
-                            v_scale=None, lse_out=None, workspace=None, num_splits: int = 0,
+                            v_scale=None, lse_out=None, workspace=None, num_ctas: int = 0,
                             stream=None, prepare=False):
     """Causal attention of each sequence's newest tokens over the paged cache
     that already holds them (pgd_paged_prefill_attention).
@@ -672,15 +672,15 @@ def paged_prefill_attention(q, k_cache, v_cache, block_table, context_lens, cu_s
     _same_device("paged_prefill_attention", q, k_cache, v_cache, block_table, context_lens,
                  cu_seqlens, k_scale, v_scale, out, lse_out, workspace)
     cap = block_table.shape[1] * block_size
-    need = prefill_workspace_bytes(B, T, max_q_len, int(max_context_len) or cap, num_q_heads,
-                                   num_kv_heads, head_dim, num_splits) if workspace is None else 0
+    need = prefill_workspace_bytes(B, T, min(max_context_len or cap, cap), window,
+                                   num_q_heads, num_kv_heads, head_dim, num_ctas) if workspace is None else 0
     ws, ws_bytes = _prefill_workspace(workspace, need, q.device, stream)
     return _issue(lib.pgd_paged_prefill_attention, "pgd_paged_prefill_attention", (
         _ptr(q), qs, _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
         _ptr(context_lens), _ptr(cu_seqlens), B, T, int(max_q_len), int(max_context_len),
         int(window), num_q_heads, num_kv_heads, head_dim, block_size, k_cache.shape[0],
         float(scale), kvd, _ptr(k_scale), _ptr(v_scale), _ptr(out), _ptr(lse_out), _ptr(ws),
-        ws_bytes, int(num_splits), _stream(stream)), prepare, out, ws)
+        ws_bytes, int(num_ctas), _stream(stream)), prepare, out, ws)
 
 
 def kv_quant_scales(k_new, v_new, k_scale: Optional[torch.Tensor] = None,

@@ -1,71 +1,117 @@
-// pgd_prefill.cu -- prompt attention, one warp per query row.
-#include "pgd_prefill.h"
-#include "pgd_prefill_rows.cuh"
+// pgd_prefill.cu -- launches of prompt attention, and the merge of cut units.
+#include "pgd_prefill.cuh"
 
 namespace pgd {
 
-constexpr int kRowWarps = 8;
+// Merge of the units that share boundaries cut.  Block (c - 1, y) looks at the
+// boundary where CTA c starts: if it is the first one inside its unit, the
+// unit's pieces are the second slot of CTA c - 1 and the first slots of CTAs
+// c, c + 1, ... as long as their starts lie inside the same unit.  One warp
+// per query row:
+//   out = sum_j exp(lse_j - M) o_j / sum_j exp(lse_j - M),  M = max_j lse_j
+constexpr int kMergeWarps = 8;
+constexpr int kMergeSplit = 8;       // blocks per boundary
+
+template <int D>
+__global__ void __launch_bounds__(32 * kMergeWarps) prefill_merge_kernel(const PrefillParams p,
+                                                                         int grid) {
+    constexpr int ROWS = D == 128 ? 256 : 128, E = D / 32;
+    const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PartRecord r = p.parts[c];
+    if (r.cut == 0) return;
+    const PartRecord before = p.parts[c - 1];
+    if (before.cut > 0 && before.unit == r.unit) return;
+    const int tpq = 128 / p.group, n = r.ntok * p.group;
+    for (int i = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); i < n;
+         i += kMergeSplit * kMergeWarps) {
+        const int tok = i / p.group, hd = i - tok * p.group;
+        const int row = tok / tpq * 128 + (tok % tpq) * p.group + hd;
+        float m = -INFINITY, l = 0.f, acc[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) acc[k] = 0.f;
+        int slot = 2 * (c - 1) + 1, cut = 0;
+        for (int j = c;; ++j) {
+            // the piece that ends where CTA j starts, or with the unit
+            int next = r.tiles;
+            bool last = true;
+            if (j < grid) {
+                const int4 x = *reinterpret_cast<const int4 *>(p.parts + j);
+                const long long unit = static_cast<long long>(static_cast<uint32_t>(x.x)) |
+                                       (static_cast<long long>(x.y) << 32);
+                if (x.z > 0 && unit == r.unit) {
+                    next = x.z;
+                    last = false;
+                }
+            }
+            if (next > cut) {
+                const int64_t pr = static_cast<int64_t>(slot) * ROWS + row;
+                const float lse = p.lse_part[pr];
+                float o[E];
+#pragma unroll
+                for (int k = 0; k < E; k += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(
+                        p.o_part + pr * D + k / 4 * 128 + lane * 4);
+                    o[k] = x.x; o[k + 1] = x.y; o[k + 2] = x.z; o[k + 3] = x.w;
+                }
+                // NaN moves neither maximum nor branch, and stays in the sums
+                if (lse != -INFINITY) {
+                    const float mn = fmaxf(m, lse);
+                    const float a = m == -INFINITY ? 0.f : expf(m - mn);
+                    const float w = expf(lse - mn);
+                    m = mn;
+                    l = l * a + w;
+#pragma unroll
+                    for (int k = 0; k < E; ++k) acc[k] = acc[k] * a + w * o[k];
+                }
+            }
+            if (last) break;
+            cut = next;
+            slot = 2 * j;
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t orow = static_cast<int64_t>(r.row0 + tok) * p.num_q_heads + r.h * p.group + hd;
+#pragma unroll
+        for (int k = 0; k < E; k += 4)
+            *reinterpret_cast<uint2 *>(p.out + orow * D + k / 4 * 128 + lane * 4) =
+                make_uint2(pack_bf16x2(acc[k] * inv, acc[k + 1] * inv),
+                           pack_bf16x2(acc[k + 2] * inv, acc[k + 3] * inv));
+        if (p.lse_out && lane == 0) p.lse_out[orow] = l == 0.f ? -INFINITY : m + logf(l);
+    }
+}
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(32 * kRowWarps) prefill_rows_kernel(const PrefillParams p) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-    if (row >= static_cast<int64_t>(p.num_tokens) * p.num_q_heads) return;
-    const int32_t tok = static_cast<int32_t>(row / p.num_q_heads);
-    const int32_t qh = static_cast<int32_t>(row % p.num_q_heads);
-    int32_t a = 0, b = p.num_seqs;                 // the sequence with cu[a] <= tok < cu[a + 1]
-    while (b - a > 1) {
-        const int32_t mid = (a + b) / 2;
-        if (__ldg(p.cu + mid) <= tok) a = mid; else b = mid;
-    }
-    const int32_t c0 = __ldg(p.cu + a), c1 = __ldg(p.cu + a + 1);
-    if (c0 < 0 || c1 < c0 || c1 > p.num_tokens) raise_flag(p.flags, kFlagContextLen);
-    if (tok < c0 || tok >= c1 || c0 < 0 || c1 > p.num_tokens) return;
-    int32_t n = c1 - c0;
-    const int h = qh / p.group;
-    KvRows kv;
-    kv.table = nullptr;
-    kv.flags = p.flags;
-    kv.head = h; kv.hkv = p.num_kv_heads; kv.bs = p.block_size; kv.num_blocks = p.num_blocks;
-    kv.row_bytes = FP8 ? D : 2 * D;
-    if (p.block_table) {
-        n = __ldg(p.context_lens + a);
-        const int32_t cap = p.max_blocks_per_seq * p.block_size;
-        if (n < 0 || n > cap) {
-            raise_flag(p.flags, kFlagContextLen);
-            n = n < 0 ? 0 : cap;
-        }
-        kv.table = p.block_table + static_cast<int64_t>(a) * p.max_blocks_per_seq;
-        kv.k = static_cast<const uint8_t *>(p.k);
-        kv.v = static_cast<const uint8_t *>(p.v);
-    } else {
-        kv.k_stride = p.k_stride * 2;
-        kv.v_stride = p.v_stride * 2;
-        kv.k = static_cast<const uint8_t *>(p.k) + c0 * kv.k_stride + h * D * 2;
-        kv.v = static_cast<const uint8_t *>(p.v) + c0 * kv.v_stride + h * D * 2;
-    }
-    const int32_t hi = n - (c1 - c0) + (tok - c0) + 1;
-    const int32_t lo = p.window > 0 ? max(0, hi - p.window) : 0;
-    const float sl2 = p.scale * 1.4426950408889634f * (FP8 ? __ldg(p.k_scale + h) : 1.f);
-    float acc[E], m, l;
-    attend_row<D, FP8>(p.q + tok * p.q_stride + qh * D, kv, lo, hi, sl2, acc, m, l);
-    const float inv = l == 0.f ? 0.f : (FP8 ? __ldg(p.v_scale + h) : 1.f) / l;
-    uint32_t *out = reinterpret_cast<uint32_t *>(p.out + row * D) + lane * (E / 2);
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i) out[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    if (p.lse_out && lane == 0)
-        p.lse_out[row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+static cudaError_t launch(const PrefillLaunch &a) {
+    using C = PrefillCfg<D, FP8>;
+    auto kernel = prefill_kernel<D, FP8>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    // the warpgroups' register shares must add up to what a CTA is launched with
+    static const bool fits = [&] {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, kernel) == cudaSuccess &&
+               f.numRegs * kPrefillThreads >= kSoftmaxRegs * 256 + kOtherRegs * 128;
+    }();
+    if (!fits) return cudaErrorLaunchOutOfResources;
+    const PrefillMaps maps = {a.map_q, a.map_k, a.map_v};
+    kernel<<<a.grid, kPrefillThreads, C::SMEM, a.stream>>>(maps, a.p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !a.p.parts || a.grid < 2) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.grid - 1, kMergeSplit);
+    cfg.blockDim = dim3(32 * kMergeWarps);
+    cfg.stream = a.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D>, a.p, a.grid);
 }
 
 cudaError_t launch_prefill(const PrefillLaunch &a) {
-    const int64_t rows = static_cast<int64_t>(a.p.num_tokens) * a.p.num_q_heads;
-    const unsigned grid = static_cast<unsigned>((rows + kRowWarps - 1) / kRowWarps);
-    auto kernel = a.p.fp8 ? prefill_rows_kernel<128, true>
-                          : a.p.head_dim == 128 ? prefill_rows_kernel<128, false>
-                                                : prefill_rows_kernel<256, false>;
-    kernel<<<grid, 32 * kRowWarps, 0, a.stream>>>(a.p);
-    return cudaGetLastError();
+    if (a.p.fp8) return launch<128, true>(a);
+    return a.p.head_dim == 128 ? launch<128, false>(a) : launch<256, false>(a);
 }
 
 }  // namespace pgd

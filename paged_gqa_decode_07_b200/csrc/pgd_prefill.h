@@ -8,6 +8,13 @@
 
 namespace pgd {
 
+// What the merge of cut units needs to know of each CTA's start.
+struct alignas(16) PartRecord {
+    long long unit;               // axis position of the unit it starts in
+    int32_t cut, tiles;           // key tile of that unit it starts at (0: not inside), of how many
+    int32_t row0, ntok, h, pad;
+};
+
 struct PrefillParams {
     const uint16_t *q;            // bf16 bits, token rows of Hq * D at q_stride
     const void *k, *v;            // packed bf16 rows, or the paged caches
@@ -17,21 +24,36 @@ struct PrefillParams {
     const float *k_scale, *v_scale;   // [Hkv] (FP8 only)
     uint16_t *out;                // bf16 bits [num_tokens][Hq][D]
     float *lse_out;               // [num_tokens][Hq] natural log, may be null
-    float *o_part;                // [splits][num_tokens][Hq][D], splits > 1 only
-    float *lse_part;              // [splits][num_tokens][Hq], natural log
+    PartRecord *parts;            // [grid]; null: units are not cut
+    float *o_part;                // [2 * grid][256 or 128 rows][D]
+    float *lse_part;              // [2 * grid][256 or 128 rows], natural log
     uint32_t *flags;
     int64_t q_stride, k_stride, v_stride;   // elements between packed tokens
     uint64_t wait_ns;
     int32_t num_seqs, num_tokens;
     int32_t num_q_heads, num_kv_heads, group, head_dim;
     int32_t max_blocks_per_seq, block_size, num_blocks;
-    int32_t window, splits, fp8;
+    int32_t window, fp8;
     float scale;
 };
 
+// Query rows of a unit: two tiles of 128 at head_dim 128, one at 256.
+inline int unit_rows(int head_dim) { return head_dim == 128 ? 256 : 128; }
+
+// Workspace of a grid whose units may be cut: the records, then the partial
+// outputs and log-sum-exps of two pieces per CTA.
+inline size_t parts_bytes(int grid) {
+    return (static_cast<size_t>(grid) * sizeof(PartRecord) + 127) / 128 * 128;
+}
+inline size_t prefill_workspace(int grid, int head_dim) {
+    const size_t rows = static_cast<size_t>(2) * grid * unit_rows(head_dim);
+    return parts_bytes(grid) + rows * head_dim * 4 + rows * 4;
+}
+
 struct PrefillLaunch {
     PrefillParams p;
-    int sms;
+    CUtensorMap map_q, map_k, map_v;
+    int grid;
     cudaStream_t stream;
 };
 

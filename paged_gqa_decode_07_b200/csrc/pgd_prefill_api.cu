@@ -1,6 +1,7 @@
 // pgd_prefill_api.cu -- the C ABI of the prompt-stage operators (declared in
 // include/pgd.h): argument checks and launches.  Nothing here synchronises
 // with the host or allocates.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 
@@ -12,6 +13,9 @@ namespace {
 using namespace pgd;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// Shares of the work that a call may ask for.
+constexpr int32_t kMaxCtas = 1024;
 
 bool supported_block(int bs) { return bs == 16 || bs == 32 || bs == 64; }
 
@@ -25,11 +29,11 @@ bool good_stride(int64_t stride, int64_t width) {
 // means that there is nothing to do.
 pgd_status check_common(int32_t num_seqs, int32_t num_tokens, int32_t max_q_len, int32_t window,
                         int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, float scale,
-                        const void *workspace, size_t workspace_bytes, int32_t num_splits,
+                        const void *workspace, size_t workspace_bytes, int32_t num_ctas,
                         bool *empty) {
     *empty = false;
     if (num_seqs < 0 || num_tokens < 0 || max_q_len < 0 || window < 0 || num_q_heads <= 0 ||
-        num_kv_heads <= 0 || num_splits < 0 || num_splits > 64)
+        num_kv_heads <= 0 || num_ctas < 0 || num_ctas > kMaxCtas)
         return PGD_ERR_INVALID_ARG;
     if (num_q_heads % num_kv_heads) return PGD_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return PGD_ERR_INVALID_ARG;
@@ -41,11 +45,80 @@ pgd_status check_common(int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
     return PGD_OK;
 }
 
-pgd_status run(PrefillLaunch &a, void *stream) {
-    const pgd_status st = device_info(&a.sms, &a.p.flags);
+// Units are cut from this many keys on (the host's bound on a sequence's).
+constexpr int64_t kCutKeys = 1024;
+
+// Grid, and whether units are cut: one CTA per SM, at most one per unit where
+// they stay whole.  Cutting costs the merge kernel (about 4 us) and evens out
+// what the longest unit would take alone (about 1 us per 128 keys).
+struct PrefillPlan {
+    int grid;
+    bool cut;
+};
+
+PrefillPlan plan_prefill(int sms, int64_t num_seqs, int64_t num_tokens, int64_t max_keys,
+                         int32_t window, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t num_ctas) {
+    if (num_ctas > 0) return {num_ctas, num_ctas > 1};
+    const int tpu = unit_rows(head_dim) / 128 * (128 / (num_q_heads / num_kv_heads));
+    const int64_t units = (num_tokens / tpu + num_seqs) * num_kv_heads;
+    // a window bounds the keys of a unit's tpu rows
+    int64_t keys = max_keys > 0 ? max_keys : INT_MAX;
+    if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + tpu);
+    if (keys >= kCutKeys) return {sms, true};
+    return {static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, units))), false};
+}
+
+pgd_status run(PrefillLaunch &a, int64_t max_keys, int32_t num_ctas, void *workspace,
+               size_t workspace_bytes, int64_t packed_rows, void *stream) {
+    PrefillParams &p = a.p;
+    int sms = 0;
+    pgd_status st = device_info(&sms, &p.flags);
     if (st != PGD_OK) return st;
-    a.p.wait_ns = wait_limit_ns();
+    PrefillPlan plan = plan_prefill(sms, p.num_seqs, p.num_tokens, max_keys, p.window,
+                                    p.num_q_heads, p.num_kv_heads, p.head_dim, num_ctas);
+    if (plan.cut && workspace_bytes < prefill_workspace(plan.grid, p.head_dim)) {
+        if (num_ctas > 0) return PGD_ERR_WORKSPACE;
+        plan.cut = false;
+    }
+    a.grid = plan.grid;
+    if (plan.cut) {
+        uint8_t *w = static_cast<uint8_t *>(workspace);
+        p.parts = reinterpret_cast<PartRecord *>(w);
+        p.o_part = reinterpret_cast<float *>(w + parts_bytes(plan.grid));
+        p.lse_part = p.o_part + static_cast<int64_t>(2) * plan.grid * unit_rows(p.head_dim) * p.head_dim;
+    }
+    p.wait_ns = wait_limit_ns();
     a.stream = static_cast<cudaStream_t>(stream);
+    // Q: 64 elements of the group's heads of 128 / g tokens
+    const uint64_t d = p.head_dim, hq = p.num_q_heads, hkv = p.num_kv_heads;
+    {
+        const uint64_t dims[3] = {d, hq, static_cast<uint64_t>(p.num_tokens)};
+        const uint64_t strides[2] = {d * 2, static_cast<uint64_t>(p.q_stride) * 2};
+        const uint32_t box[3] = {64, static_cast<uint32_t>(p.group),
+                                 static_cast<uint32_t>(128 / p.group)};
+        st = encode_tiled_map(&a.map_q, p.q, 2, 3, dims, strides, box);
+        if (st != PGD_OK) return st;
+    }
+    for (int i = 0; i < 2; ++i) {
+        CUtensorMap *m = i ? &a.map_v : &a.map_k;
+        const void *base = i ? p.v : p.k;
+        if (p.block_table) {
+            // a block of one head: 128-byte lines of its rows
+            const uint64_t bs = p.block_size, eb = p.fp8 ? 1 : 2, line = 128 / eb;
+            const uint64_t dims[4] = {line, bs, d / line, static_cast<uint64_t>(p.num_blocks) * hkv};
+            const uint64_t strides[3] = {d * eb, 128, bs * d * eb};
+            const uint32_t box[4] = {static_cast<uint32_t>(line), static_cast<uint32_t>(bs), 1, 1};
+            st = encode_tiled_map(m, base, static_cast<int>(eb), 4, dims, strides, box);
+        } else {
+            const int64_t stride = i ? p.v_stride : p.k_stride;
+            const uint64_t dims[3] = {d, hkv, static_cast<uint64_t>(packed_rows)};
+            const uint64_t strides[2] = {d * 2, static_cast<uint64_t>(stride) * 2};
+            const uint32_t box[3] = {64, 1, 128};
+            st = encode_tiled_map(m, base, 2, 3, dims, strides, box);
+        }
+        if (st != PGD_OK) return st;
+    }
     return launch_prefill(a) == cudaSuccess ? PGD_OK : PGD_ERR_CUDA;
 }
 
@@ -53,12 +126,20 @@ pgd_status run(PrefillLaunch &a, void *stream) {
 
 extern "C" {
 
-size_t pgd_prefill_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
-                                   int32_t max_context_len, int32_t num_q_heads,
-                                   int32_t num_kv_heads, int32_t head_dim, int32_t num_splits) {
-    (void)num_seqs; (void)num_tokens; (void)max_q_len; (void)max_context_len;
-    (void)num_q_heads; (void)num_kv_heads; (void)head_dim; (void)num_splits;
-    return 0;
+size_t pgd_prefill_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t max_context_len,
+                                   int32_t window, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t num_ctas) {
+    bool empty;
+    if (max_context_len < 0 ||
+        check_common(num_seqs, num_tokens, 0, window, num_q_heads, num_kv_heads, head_dim, 1.f,
+                     nullptr, 0, num_ctas, &empty) != PGD_OK || empty)
+        return 0;
+    int sms = 0;
+    uint32_t *flags = nullptr;
+    if (device_info(&sms, &flags) != PGD_OK) return 0;
+    const PrefillPlan plan = plan_prefill(sms, num_seqs, num_tokens, max_context_len, window,
+                                          num_q_heads, num_kv_heads, head_dim, num_ctas);
+    return plan.cut ? prefill_workspace(plan.grid, head_dim) : 0;
 }
 
 pgd_status pgd_prefill_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
@@ -66,12 +147,12 @@ pgd_status pgd_prefill_attention(const void *q, int64_t q_stride, const void *k,
                                  int32_t num_seqs, int32_t num_tokens, int32_t max_seq_len,
                                  int32_t window, int32_t num_q_heads, int32_t num_kv_heads,
                                  int32_t head_dim, float scale, void *out, float *lse_out,
-                                 void *workspace, size_t workspace_bytes, int32_t num_splits,
+                                 void *workspace, size_t workspace_bytes, int32_t num_ctas,
                                  void *stream) {
     bool empty;
     pgd_status st = check_common(num_seqs, num_tokens, max_seq_len, window, num_q_heads,
                                  num_kv_heads, head_dim, scale, workspace, workspace_bytes,
-                                 num_splits, &empty);
+                                 num_ctas, &empty);
     if (st != PGD_OK || empty) return st;
     if (!q || !k || !v || !cu_seqlens || !out) return PGD_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
@@ -97,11 +178,11 @@ pgd_status pgd_prefill_attention(const void *q, int64_t q_stride, const void *k,
     p.group = num_q_heads / num_kv_heads;
     p.head_dim = head_dim;
     p.window = window;
-    p.splits = 1;
     p.scale = scale;
     p.out = static_cast<uint16_t *>(out);
     p.lse_out = lse_out;
-    return run(a, stream);
+    const int64_t keys = max_seq_len > 0 && max_seq_len < num_tokens ? max_seq_len : num_tokens;
+    return run(a, keys, num_ctas, workspace, workspace_bytes, num_tokens, stream);
 }
 
 pgd_status pgd_paged_prefill_attention(
@@ -111,11 +192,11 @@ pgd_status pgd_paged_prefill_attention(
     int32_t max_context_len, int32_t window, int32_t num_q_heads, int32_t num_kv_heads,
     int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale, pgd_kv_dtype kv_dtype,
     const float *k_scale, const float *v_scale, void *out, float *lse_out, void *workspace,
-    size_t workspace_bytes, int32_t num_splits, void *stream) {
+    size_t workspace_bytes, int32_t num_ctas, void *stream) {
     bool empty;
     pgd_status st = check_common(num_seqs, num_tokens, max_q_len, window, num_q_heads,
                                  num_kv_heads, head_dim, scale, workspace, workspace_bytes,
-                                 num_splits, &empty);
+                                 num_ctas, &empty);
     if (st != PGD_OK) return st;
     if (max_blocks_per_seq <= 0 || num_blocks <= 0 || max_context_len < 0)
         return PGD_ERR_INVALID_ARG;
@@ -158,11 +239,13 @@ pgd_status pgd_paged_prefill_attention(
     p.group = num_q_heads / num_kv_heads;
     p.head_dim = head_dim;
     p.window = window;
-    p.splits = 1;
     p.scale = scale;
     p.out = static_cast<uint16_t *>(out);
     p.lse_out = lse_out;
-    return run(a, stream);
+    // the table's width bounds every context
+    const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * block_size;
+    const int64_t keys = max_context_len > 0 && max_context_len < cap ? max_context_len : cap;
+    return run(a, keys, num_ctas, workspace, workspace_bytes, 0, stream);
 }
 
 // The row kernels index a token's chunks with 32-bit integers.

@@ -124,17 +124,17 @@ def test_growing_scores_move_the_reference_every_tile():
         prefill_ref.assert_within(out, lse, prefill_ref.packed(q, k, v, cu, 0, sc), T, d, "bf16")
 
 
-@pytest.mark.parametrize("splits", [1, 2, 3, 7, 64])
+@pytest.mark.parametrize("ctas", [1, 2, 3, 7, 64, 500])
 @pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (8, 1, 256)])
-def test_split_counts(splits, hq, hkv, d):
-    check_packed([700, 0, 1, 300], hq, hkv, d, num_splits=splits, gap=2, tail=3)
-    check_packed([1100], hq, hkv, d, num_splits=splits, window=200)
+def test_cut_work(ctas, hq, hkv, d):
+    check_packed([700, 0, 1, 300], hq, hkv, d, num_ctas=ctas, gap=2, tail=3)
+    check_packed([1100], hq, hkv, d, num_ctas=ctas, window=200)
 
 
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("d", [128, 256])
-@pytest.mark.parametrize("splits", [1, 2])
-def test_masked_keys_have_no_influence(bad, d, splits):
+@pytest.mark.parametrize("ctas", [1, 2])
+def test_masked_keys_have_no_influence(bad, d, ctas):
     """A non-finite key or value reaches the rows that see it and no other."""
     T, hq, hkv, at, window = 300, 8, 2, 137, 90
     q, k, v = (randn((T, h, d), 20 + i) for i, h in enumerate((hq, hkv, hkv)))
@@ -145,7 +145,7 @@ def test_masked_keys_have_no_influence(bad, d, splits):
     for which in ("k", "v"):
         kk, vv = k.clone(), v.clone()
         (kk if which == "k" else vv)[at, 1, 5] = bad
-        out, lse = run_packed(q, kk, vv, cu_t, hq, hkv, d, 0.09, window=window, num_splits=splits)
+        out, lse = run_packed(q, kk, vv, cu_t, hq, hkv, d, 0.09, window=window, num_ctas=ctas)
         keep = [r[~sees] for r in ref]
         prefill_ref.assert_within(out[~sees], lse[~sees], keep, T, d, "bf16", which)
         other = [r[sees][:, :hq // 2] for r in ref]   # the heads of KV head 0
@@ -279,15 +279,15 @@ def test_paged_windows(window, d, dt):
     check_paged([40, 1, 260], [700, 333, 260], 8, 2, d, 32, dt, window=window, seed=6)
 
 
-@pytest.mark.parametrize("splits", [1, 2, 5, 64])
+@pytest.mark.parametrize("ctas", [1, 2, 5, 64, 500])
 @pytest.mark.parametrize("d,dt", [(128, "bf16"), (256, "bf16"), (128, "e4m3")])
-def test_paged_split_counts(splits, d, dt):
-    check_paged([3, 1, 65, 0], [1500, 16, 700, 9], 8, 2, d, 16, dt, seed=7, num_splits=splits,
+def test_paged_cut_work(ctas, d, dt):
+    check_paged([3, 1, 65, 0], [1500, 16, 700, 9], 8, 2, d, 16, dt, seed=7, num_ctas=ctas,
                 gap=1, tail=2)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "e4m3"])
-def test_paged_without_hints_and_automatic_splits(dt):
+def test_paged_without_hints_and_automatic_grid(dt):
     check_paged([30], [6000], 8, 1, 128, 16, dt, seed=8, hints=False)
     check_paged([30], [6000], 8, 1, 128, 16, dt, seed=8)
 
@@ -405,17 +405,17 @@ def test_repeats_other_streams_prepared_calls_and_graphs_agree():
     lens, hq, hkv, d = [300, 1, 77], 8, 2, 128
     cu, cu_t = cu_of(lens)
     q, k, v = (randn((cu[-1], h, d), 90 + i) for i, h in enumerate((hq, hkv, hkv)))
-    first, first_lse = run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_splits=2)
-    again, again_lse = run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_splits=2)
+    first, first_lse = run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_ctas=2)
+    again, again_lse = run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_ctas=2)
     assert torch.equal(bits(first), bits(again)) and torch.equal(bits(first_lse), bits(again_lse))
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     other = torch.zeros_like(first)
-    pgd.prefill_attention(q, k, v, cu_t, hq, hkv, d, 0.09, other, num_splits=2, stream=s)
+    pgd.prefill_attention(q, k, v, cu_t, hq, hkv, d, 0.09, other, num_ctas=2, stream=s)
     s.synchronize()
     assert torch.equal(bits(first), bits(other))
     out = torch.zeros_like(first)
-    call = pgd.prefill_attention(q, k, v, cu_t, hq, hkv, d, 0.09, out, num_splits=2, prepare=True)
+    call = pgd.prefill_attention(q, k, v, cu_t, hq, hkv, d, 0.09, out, num_ctas=2, prepare=True)
     for _ in range(3):
         out.zero_()
         assert call() is out
@@ -427,11 +427,11 @@ def test_repeats_other_streams_prepared_calls_and_graphs_agree():
         o = torch.zeros_like(first)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            pgd.prefill_attention(q, k, v, cu_t, hq, hkv, d, 0.09, o, num_splits=2)
+            pgd.prefill_attention(q, k, v, cu_t, hq, hkv, d, 0.09, o, num_ctas=2)
         graphs.append(g)
         outs.append(o)
     q.copy_(randn(q.shape, 99))
-    want, _ = run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_splits=2)
+    want, _ = run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_ctas=2)
     for g in graphs + graphs:
         g.replay()
     torch.cuda.synchronize()
@@ -446,14 +446,14 @@ def test_two_streams_at_once():
     cu, cu_t = cu_of(lens)
     data = [[randn((900, h, d), 100 + 5 * j + i) for i, h in enumerate((hq, hkv, hkv))]
             for j in range(2)]
-    want = [run_packed(*x, cu_t, hq, hkv, d, 0.09, num_splits=3)[0] for x in data]
+    want = [run_packed(*x, cu_t, hq, hkv, d, 0.09, num_ctas=3)[0] for x in data]
     streams = [torch.cuda.Stream() for _ in range(2)]
     outs = [torch.zeros_like(w) for w in want]
     torch.cuda.synchronize()
     for _ in range(10):
         for j in range(2):
             with torch.cuda.stream(streams[j]):
-                pgd.prefill_attention(*data[j], cu_t, hq, hkv, d, 0.09, outs[j], num_splits=3)
+                pgd.prefill_attention(*data[j], cu_t, hq, hkv, d, 0.09, outs[j], num_ctas=3)
     torch.cuda.synchronize()
     for o, w in zip(outs, want):
         assert torch.equal(bits(o), bits(w))
@@ -478,16 +478,16 @@ def test_workspace_is_checked_and_used():
     lens, hq, hkv, d = [900], 8, 2, 128
     cu, cu_t = cu_of(lens)
     q, k, v = (randn((900, h, d), 120 + i) for i, h in enumerate((hq, hkv, hkv)))
-    need = pgd.prefill_workspace_bytes(1, 900, 900, 900, hq, hkv, d, 3)
+    need = pgd.prefill_workspace_bytes(1, 900, 900, 0, hq, hkv, d, 3)
     assert need > 0
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-    want, _ = run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_splits=3)
-    got, _ = run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_splits=3, workspace=ws)
+    want, _ = run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_ctas=3)
+    got, _ = run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_ctas=3, workspace=ws)
     assert torch.equal(bits(want), bits(got))
     with pytest.raises(pgd.PGDError) as e:
-        run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_splits=3, workspace=ws[:need // 2])
+        run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_ctas=3, workspace=ws[:need // 2])
     assert e.value.status == 6
-    # an automatic count runs with what fits
+    # without enough of it an automatic call cuts nothing
     out, lse = run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, workspace=ws[:16])
     prefill_ref.assert_within(out, lse, prefill_ref.packed(q, k, v, cu, 0, 0.09), 900, d, "bf16")
 

@@ -38,7 +38,7 @@ def prefill(lib, **kw):
     (dict(Hq=6, Hkv=4), INVALID), (dict(Hq=34, Hkv=2, qs=4352), UNSUPPORTED),
     (dict(D=64), UNSUPPORTED), (dict(D=96), UNSUPPORTED), (dict(Hkv=0), INVALID),
     (dict(B=-1), INVALID), (dict(T=-1), INVALID), (dict(W=-1), INVALID), (dict(ml=-1), INVALID),
-    (dict(ns=-1), INVALID), (dict(ns=65), INVALID),
+    (dict(ns=-1), INVALID), (dict(ns=1025), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID),
     (dict(cu=None), INVALID), (dict(out=None), INVALID),
