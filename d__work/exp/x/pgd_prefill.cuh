@@ -1,0 +1,969 @@
+// pgd_prefill.cuh -- prompt attention on the 5th-generation tensor cores.
+//
+// What it computes ("attention kernels", froggydisk: sections "standard
+// attention", "FlashAttention", "paged KV and kernels"): for every query row
+// (token i, head a) of every sequence
+//     out = softmax(scale * q . K_t) V_t  over the visible positions t,
+// causal, optionally the last `window` of them, K/V packed or in pages.
+//
+// Tiles.  A query tile is 128 rows of one KV head: the g heads of its group
+// for 128 / g consecutive tokens, so K/V is read once per group and the causal
+// diagonal is only 128 / g tokens wide.  A unit is NQ query tiles (2 at
+// head_dim 128, 1 at 256) and all keys that they see; keys come in tiles of 128.
+//
+// Work.  The units of all sequences laid end to end, each as long as its keys
+// plus a constant, are cut into one equal share per CTA (pgd_prefill_sched.cuh).
+// A unit that a boundary cuts leaves one unrounded piece per CTA in the
+// workspace; a second kernel merges them by log-sum-exp.
+//
+// CTA = 2 softmax warpgroups + one of four single warps:
+//   warps 0-3, 4-7   softmax; thread = query row (one TMEM lane)
+//   warp 8           finds the share, hands its pieces out, and loads: Q and
+//                    [128 keys x 128 dims] boxes of K and V into a ring (TMA)
+//   warp 9           issues the tcgen05.mma of S = Q K^T and O += P V
+//   warps 10, 11     keep masked keys out of V (below); for FP8 caches they
+//                    also turn the E4M3 boxes and the query rows into f16
+// S, P and O live in tensor memory (512 columns):
+//   NQ = 2: S0 | S1 | O0 | O1, P_t in the columns of S_t.  The two tiles take
+//     turns: one's softmax runs while the other's products do, and S_t(j + 1)
+//     follows P_t(j) V(j) in issue order, so S_t ready means O_t is at rest.
+//   NQ = 1: S0 | S1 | O (256): S(j + 1) is formed while softmax(j) runs.
+//
+// Softmax, one pass with a running reference m and sum l in fp32: the weights
+// are p = 2^(x - m), and m moves (O and l rescaled) only when a score exceeds
+// it by more than 8 (weights stay below 2^8, O below 2^8 times its value).
+// P enters the product as bf16 (f16 for FP8 caches, whose V is exact there);
+// l sums the unrounded weights.
+//
+// Masked keys.  A masked weight is zero, but zero times a V row that is not
+// finite is NaN, and rows of unowned slots may hold anything.  On key tiles
+// that some row does not fully see, the V warps zero the rows no query of the
+// unit sees before the product reads them, and look for non-finite values in
+// the rest; where there is one, the unit's rows are computed again one warp
+// per row from the definition (attend_row), which touches visible keys only.
+//
+// Every wait is bounded (wait_ns): a role that gives up raises the timeout
+// flag and leaves; the producer and the MMA warp then wait for what they have
+// in flight, all warps meet, and tensor memory is freed.
+#pragma once
+
+#include "pgd_prefill_rows.cuh"
+#include "pgd_prefill_sched.cuh"
+#include "pgd_umma.cuh"
+
+namespace pgd {
+
+constexpr uint32_t kLine = 128 * 128;         // bytes of a line: 128 rows x 128 B
+constexpr uint32_t kBox = 2 * kLine;          // [128 keys][128 dims], 16-bit
+constexpr uint32_t kRawBox = kLine;           // [128 keys][128 dims], 8-bit
+// Of every 8 pairs of exponentials, how many are computed with FMAs.
+constexpr int kPolyOf8 = 2;
+constexpr int kRedoSlots = 8;
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;   // 8 warps and 4: 12 x 168 in all
+constexpr uint32_t kMetaBytes = 1024;
+
+template <int D, bool FP8>
+struct PrefillCfg {
+    static constexpr int NQ = D == 128 ? 2 : 1;
+    static constexpr int LINES = D / 64;              // lines of a Q tile
+    static constexpr int BOXES = D / 128;             // boxes of a K or V tile
+    static constexpr uint32_t QTILE = LINES * kLine;
+    static constexpr int NS = FP8 ? 3 : 4;            // ring of 16-bit boxes
+    static constexpr int NR = FP8 ? 2 : 0;            // ring of raw E4M3 boxes
+    static constexpr uint32_t STAGE = NQ * 4 * 4096;  // outputs on their way out, 4 KB a warp
+    static constexpr uint32_t OFF_RING = NQ * QTILE;
+    static constexpr uint32_t OFF_RAW = OFF_RING + NS * kBox;
+    static constexpr uint32_t OFF_STAGE = OFF_RAW + NR * kRawBox;
+    static constexpr uint32_t OFF_META = OFF_STAGE + STAGE;
+    static constexpr uint32_t SMEM = OFF_META + kMetaBytes + (FP8 ? 2048 : 0);
+    static_assert(SMEM <= 232448, "more shared memory than a CTA has");
+};
+
+// Barriers and small state behind the tiles (for FP8, 2 x 256 multipliers of
+// the query rows follow).
+struct PrefillMeta {
+    uint64_t q_full, q_ready, q_empty, drain, pv_done;
+    uint64_t s_ready[2], p_ready[2][2], o_done[2], o_free[2];
+    uint64_t full[4], empty[4], fixed[4];
+    uint64_t raw_full[3], raw_empty[3];
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
+    Piece piece[kPieces];
+    Share share;
+    uint32_t tmem, redo[kRedoSlots];
+};
+static_assert(sizeof(PrefillMeta) <= kMetaBytes, "PrefillMeta grew");
+
+struct PrefillMaps {
+    CUtensorMap q, k, v;
+};
+
+// The keys that each query tile of a piece sees.
+struct TileKeys {
+    int ntok;           // query tokens of the tile
+    int p0;             // position of the first
+    int kb, ke;         // key tiles of this piece
+    int mlo, mhi;       // tiles below mlo or from mhi on are not seen whole by every row
+};
+
+template <int NQ>
+struct UnitKeys {
+    TileKeys t[NQ];
+    int kb, ke;
+    int lo, hi;         // positions that some row sees (whole unit)
+    int all_lo, all_hi; // positions that every row sees
+    int part_lo, part_hi;
+
+    __device__ __forceinline__ bool active(int i, int j) const {
+        return j >= t[i].kb && j < t[i].ke;
+    }
+    // whether some row of query tile i does not see all of key tile j
+    __device__ __forceinline__ bool masked(int i, int j) const {
+        return j < t[i].mlo || j >= t[i].mhi;
+    }
+    // the same for the unit's active tiles (their ranges leave no gap)
+    __device__ __forceinline__ bool partial(int j) const { return j < part_lo || j >= part_hi; }
+};
+
+template <int NQ>
+__device__ __forceinline__ UnitKeys<NQ> unit_keys(const PrefillParams &p, const Piece &u, int tpq) {
+    UnitKeys<NQ> k;
+    k.kb = u.kb;
+    k.ke = u.ke;
+    k.hi = u.pos0 + u.ntok;
+    k.lo = p.window > 0 ? max(0, u.pos0 + 1 - p.window) : 0;
+    k.all_hi = u.pos0 + 1;
+    k.all_lo = p.window > 0 ? k.hi - p.window : 0;
+    k.part_lo = 0;
+    k.part_hi = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        TileKeys &t = k.t[i];
+        t.ntok = min(tpq, u.ntok - i * tpq);
+        t.p0 = u.pos0 + i * tpq;
+        t.kb = t.ke = t.mlo = t.mhi = 0;
+        const int hi = t.p0 + t.ntok;
+        if (t.ntok > 0 && hi > 0) {
+            t.kb = max(p.window > 0 ? max(0, t.p0 + 1 - p.window) / kKeys : 0, u.kb);
+            t.ke = max(t.kb, min((hi + kKeys - 1) / kKeys, u.ke));
+            t.mlo = p.window > 0 ? (max(0, hi - p.window) + kKeys - 1) / kKeys : 0;
+            t.mhi = max(0, t.p0 + 1) / kKeys;
+            k.part_lo = max(k.part_lo, t.mlo);
+            k.part_hi = min(k.part_hi, t.mhi);
+        }
+    }
+    return k;
+}
+
+// ---------------------------------------------------------------- the V warps
+// Keep masked keys out of a 16-bit V box: zero the rows outside [lo, hi) of
+// the tile's keys, and tell whether one that only some query rows see, outside
+// [all_lo, all_hi), holds a non-finite value.  64 threads, 8 of them on one
+// row's 128-byte line.
+__device__ __forceinline__ bool clean_box(uint32_t box, int lo, int hi, int all_lo, int all_hi,
+                                          int tid) {
+    bool bad = false;
+    const uint32_t at = box + (tid & 7) * 16;
+    const int r0 = tid >> 3;
+    for (int r = r0; r < 128; r += 8) {
+        if (r >= all_lo && r < all_hi) continue;
+        const uint32_t a = at + r * 128;
+        if (r < lo || r >= hi) {
+            sts128(a, 0, 0, 0, 0);
+            sts128(a + kLine, 0, 0, 0, 0);
+        } else {
+            uint32_t x[8];
+            lds128(a, x[0], x[1], x[2], x[3]);
+            lds128(a + kLine, x[4], x[5], x[6], x[7]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                bad |= (((x[k] & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u) != 0;
+        }
+    }
+    return bad;
+}
+
+// A raw E4M3 box to f16 (both with the 128-byte swizzle); as clean_box for
+// rows outside [lo, hi), which become zeros without being looked at.
+__device__ __forceinline__ bool convert_box(uint32_t raw, uint32_t box, int lo, int hi, int tid) {
+    bool bad = false;
+#pragma unroll 4
+    for (int i = tid; i < 128 * 8; i += 64) {
+        const int r = i >> 3, c = i & 7, sw = r & 7;
+        uint32_t x[4];
+        lds128(raw + r * 128 + ((c ^ sw) << 4), x[0], x[1], x[2], x[3]);
+        if (r < lo || r >= hi) {
+            x[0] = x[1] = x[2] = x[3] = 0;
+        }
+        uint32_t y[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            bad |= (((x[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+            y[2 * k] = e4m3x2_to_f16x2(x[k] & 0xFFFFu);
+            y[2 * k + 1] = e4m3x2_to_f16x2(x[k] >> 16);
+        }
+        // 16 elements: two chunks of line c / 4; lanes of the second line
+        // write theirs in the other order, so that a row's eight lanes hit
+        // eight different chunk positions
+        const uint32_t row = box + (c >> 2) * kLine + r * 128;
+        const int o = (c & 3) * 2, f = c >> 2;
+        const uint32_t a0 = row + (((o + f) ^ sw) << 4), a1 = row + (((o + 1 - f) ^ sw) << 4);
+        if (f) {
+            sts128(a0, y[4], y[5], y[6], y[7]);
+            sts128(a1, y[0], y[1], y[2], y[3]);
+        } else {
+            sts128(a0, y[0], y[1], y[2], y[3]);
+            sts128(a1, y[4], y[5], y[6], y[7]);
+        }
+    }
+    return bad;
+}
+
+// A query row (one thread), bf16 -> f16 in place, multiplied by the power of
+// two that brings its largest element to [2^14, 2^15): exact for every element
+// within 2^-28 of it.  Returns the inverse power (1 for a row of zeros or
+// one that is not finite).
+__device__ __forceinline__ float convert_q_row(uint32_t tile, int r) {
+    const uint32_t sw = r & 7;
+    uint32_t m = 0;
+    for (int c = 0; c < 16; ++c) {
+        uint32_t x[4];
+        lds128(tile + (c >> 3) * kLine + r * 128 + (((c & 7) ^ sw) << 4), x[0], x[1], x[2], x[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = __vmaxu2(m, x[k] & 0x7FFF7FFFu);
+    }
+    const uint32_t top = max(m & 0xFFFFu, m >> 16);
+    int e = static_cast<int>(top >> 7) - 127;            // floor(log2) of a normal
+    if (top == 0 || top >= 0x7F80u) e = 14;
+    if (e < -110) e = -110;                              // keep both powers normal
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+    for (int c = 0; c < 16; ++c) {
+        const uint32_t a = tile + (c >> 3) * kLine + r * 128 + (((c & 7) ^ sw) << 4);
+        uint32_t x[4];
+        lds128(a, x[0], x[1], x[2], x[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = unpack_bf16x2(x[k]);
+            x[k] = pack_f16x2(f.x * up, f.y * up);
+        }
+        sts128(a, x[0], x[1], x[2], x[3]);
+    }
+    return __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+}
+
+// ---------------------------------------------------------------- softmax
+// max(a, b, c), NaN if one is
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 2^x of a pair (x <= 9, or NaN, whose result is any number: the row's sum is
+// NaN already).  x = n + f with n the nearest integer, read off the low bits
+// of x + 1.5 * 2^23; 2^f on [-1/2, 1/2] by the polynomial of degree 5 with
+// constant term 1 and the least largest relative error (fitted by linear
+// programming; 2^-22.5 with its fp32 roundings), n added to the exponent.  At
+// the clamp, x = -127, f is 0 and the sum of the bits is 0 exactly: what a
+// mask set to -infinity weighs nothing.
+__device__ __forceinline__ float2 exp2_poly2(float2 x) {
+    const float2 magic = make_float2(12582912.f, 12582912.f), back = make_float2(-12582912.f, -12582912.f);
+    x.x = fmaxf(x.x, -127.f);
+    x.y = fmaxf(x.y, -127.f);
+    const float2 n = add2(x, magic);
+    const float2 f = fma2(add2(n, back), make_float2(-1.f, -1.f), x);
+    float2 q = make_float2(0.001326472731307149f, 0.001326472731307149f);
+    q = fma2(q, f, make_float2(0.009671512991189957f, 0.009671512991189957f));
+    q = fma2(q, f, make_float2(0.05550733581185341f, 0.05550733581185341f));
+    q = fma2(q, f, make_float2(0.24022242426872253f, 0.24022242426872253f));
+    q = fma2(q, f, make_float2(0.6931470036506653f, 0.6931470036506653f));
+    q = fma2(q, f, make_float2(1.f, 1.f));
+    return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(n.x) << 23)),
+                       __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(n.y) << 23)));
+}
+
+// ---------------------------------------------------------------- the kernel
+// A warp's wait for a phase, all lanes or none: false when `limit_ns` ran out
+// (the timeout flag is raised).  One short loop: the kernel's loops run from
+// the small instruction caches, and there are many waits.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                          uint32_t *flags) {
+    const uint32_t nap = limit_ns < 20000 ? static_cast<uint32_t>(limit_ns) : 20000u;
+    uint64_t t0 = 0;
+    while (!__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, nap))) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, now - t0 > limit_ns)) {
+            raise_flag(flags, kFlagTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kPrefillThreads, 1)
+prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) {
+    using C = PrefillCfg<D, FP8>;
+    constexpr int NQ = C::NQ;
+    extern __shared__ __align__(1024) uint8_t smem_al[];
+    const uint32_t smem = smem_u32(smem_al);
+    if (smem & 1023) {                           // the swizzled boxes start on 1024 bytes
+        if (threadIdx.x == 0) raise_flag(p.flags, kFlagTimeout);
+        return;
+    }
+    PrefillMeta &meta = *reinterpret_cast<PrefillMeta *>(smem_al + C::OFF_META);
+    float *row_mult = reinterpret_cast<float *>(smem_al + C::OFF_META + kMetaBytes);
+    const uint32_t ring = smem + C::OFF_RING, raw_ring = smem + C::OFF_RAW;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const auto bar = [](uint64_t &b) { return smem_u32(&b); };
+
+    if (threadIdx.x == 0) {
+        mbar_init(bar(meta.q_full), 1);
+        mbar_init(bar(meta.q_ready), 2);
+        mbar_init(bar(meta.q_empty), 1);
+        mbar_init(bar(meta.drain), 1);
+        mbar_init(bar(meta.pv_done), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(meta.s_ready[i]), 1);
+            mbar_init(bar(meta.p_ready[i][0]), 4);
+            mbar_init(bar(meta.p_ready[i][1]), 4);
+            mbar_init(bar(meta.o_done[i]), 1);
+            mbar_init(bar(meta.o_free[i]), 4);
+        }
+        for (int i = 0; i < 4; ++i) {
+            // 16-bit ring: filled by TMA and read by the MMA and the V warps,
+            // or (FP8) filled by the two V warps and read by the MMA
+            mbar_init(bar(meta.full[i]), FP8 ? 2 : 1);
+            mbar_init(bar(meta.empty[i]), FP8 ? 1 : 3);
+            mbar_init(bar(meta.fixed[i]), 2);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(bar(meta.raw_full[i]), 1);
+            mbar_init(bar(meta.raw_empty[i]), 2);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(bar(meta.piece_full[i]), 1);
+            mbar_init(bar(meta.piece_empty[i]), 3 + 4 * NQ);   // MMA, V and softmax warps
+        }
+        for (int i = 0; i < kRedoSlots; ++i) meta.redo[i] = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&maps.q);
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
+    }
+    if (warp == 9) tmem_alloc(smem_u32(&meta.tmem), 512);
+    find_share<NQ>(p, meta.share);               // meets at __syncthreads
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    constexpr uint32_t tmem = 0;                 // all 512 columns start at the first
+    constexpr uint32_t kOCol = 256;              // O_t at kOCol + t * 128
+    const int tpq = 128 / p.group;
+    const uint64_t limit = p.wait_ns;
+    Piece u;
+    int piece = 0;
+
+    const auto wait = [&](uint64_t &b, uint32_t parity) {
+        return warp_wait(smem_u32(&b), parity, limit, p.flags);
+    };
+    // the next piece handed out by the producer; false at the end
+    const auto next_piece = [&]() {
+        const int s = piece % kPieces;
+        if (!wait(meta.piece_full[s], (piece / kPieces) & 1)) return false;
+        ++piece;
+        u = meta.piece[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(meta.piece_empty[s]));
+        return u.ntok > 0;
+    };
+
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 8) {
+        // ================================================== producer
+        constexpr int N = FP8 ? C::NR : C::NS;
+        uint64_t *full = FP8 ? meta.raw_full : meta.full;
+        uint64_t *empty = FP8 ? meta.raw_empty : meta.empty;
+        const uint32_t base = FP8 ? raw_ring : ring;
+        const bool paged = p.block_table != nullptr;
+        const int bs = p.block_size;
+        const int nblk = paged ? kKeys / bs : 1;
+        int boxes = 0, units = 0;
+        bool ok = true;
+        PieceWalk<NQ> walk(p, meta.share);
+        while (ok) {
+            const bool more = walk.next(u);
+            if (!more) u.ntok = 0;
+            if (!(ok = wait(meta.piece_empty[piece % kPieces], ((piece / kPieces) & 1) ^ 1))) break;
+            if (lane == 0) {
+                meta.piece[piece % kPieces] = u;
+                mbar_arrive(bar(meta.piece_full[piece % kPieces]));
+            }
+            ++piece;
+            if (!more) break;
+            const UnitKeys<NQ> k = unit_keys<NQ>(p, u, tpq);
+            if (k.kb >= k.ke) continue;
+            const int32_t *table = p.block_table + static_cast<int64_t>(u.seq) * p.max_blocks_per_seq;
+            // block ids of key tile j: lane b % nblk holds block b's (or -1)
+            const auto ids = [&](int j) {
+                if (!paged || j >= k.ke) return -1;
+                const int key = j * kKeys + (lane % nblk) * bs;
+                if (key + bs <= k.lo || key >= k.hi) return -1;
+                int id = __ldg(table + key / bs);
+                if (id < 0 || id >= p.num_blocks) {
+                    raise_flag(p.flags, kFlagBlockId);
+                    id = 0;
+                }
+                return id;
+            };
+            const auto load = [&](const CUtensorMap *map, int j, int half, int id) {
+                const int s = boxes % N;
+                if (!wait(empty[s], ((boxes / N) & 1) ^ 1)) return false;
+                ++boxes;
+                const uint32_t b = smem_u32(&full[s]);
+                const uint32_t dst = base + s * (FP8 ? kRawBox : kBox);
+                if (!paged) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(b, kBox);
+#pragma unroll
+                        for (int l = 0; l < 2; ++l)
+                            tma_load_3d(dst + l * kLine, map, b, (2 * half + l) * 64, u.h,
+                                        u.kv0 + j * kKeys);
+                    }
+                } else {
+                    constexpr int L = FP8 ? 1 : 2;       // loads per block
+                    const bool mine = lane < nblk * L && id >= 0;
+                    const int cnt = __popc(__ballot_sync(0xffffffffu, mine));
+                    if (lane == 0) mbar_arrive_expect_tx(b, cnt * bs * 128);
+                    __syncwarp();
+                    if (mine) {
+                        const int l = lane / nblk;
+                        tma_load_4d(dst + l * kLine + (lane % nblk) * bs * 128, map, b, 0, 0,
+                                    FP8 ? 0 : 2 * half + l, id * p.num_kv_heads + u.h);
+                    }
+                }
+                __syncwarp();
+                return true;
+            };
+            int id = ids(k.kb), id_next = ids(k.kb + 1);
+            if (!(ok = wait(meta.q_empty, (units & 1) ^ 1))) break;
+            ++units;
+            if (lane == 0) {
+                const uint32_t b = bar(meta.q_full);
+                int tiles = 0;
+                for (int i = 0; i < NQ; ++i) tiles += k.t[i].ntok > 0;
+                mbar_arrive_expect_tx(b, tiles * C::LINES * tpq * p.group * 128);
+                for (int i = 0; i < tiles; ++i)
+                    for (int l = 0; l < C::LINES; ++l)
+                        tma_load_3d(smem + i * C::QTILE + l * kLine, &maps.q, b, l * 64,
+                                    u.h * p.group, u.row0 + i * tpq);
+            }
+            __syncwarp();
+            if (NQ == 2) {
+                for (int j = k.kb; ok && j < k.ke; ++j) {
+                    const int id2 = ids(j + 2);
+                    ok = load(&maps.k, j, 0, id) && load(&maps.v, j, 0, id);
+                    id = id_next;
+                    id_next = id2;
+                }
+            } else {
+                for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.k, k.kb, b, id);
+                for (int j = k.kb; ok && j < k.ke; ++j) {
+                    const int id2 = ids(j + 2);
+                    if (j + 1 < k.ke)
+                        for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.k, j + 1, b, id_next);
+                    for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.v, j, b, id);
+                    id = id_next;
+                    id_next = id2;
+                }
+            }
+        }
+        // every copy must land before the CTA exits
+        bool landed = true;
+        for (int i = max(0, boxes - N); i < boxes; ++i)
+            landed &= mbar_wait_bounded(smem_u32(&full[i % N]), (i / N) & 1, kDrainWaitNs);
+        if (units > 0)
+            landed &= mbar_wait_bounded(bar(meta.q_full), (units - 1) & 1, kDrainWaitNs);
+        if (!landed) raise_flag(p.flags, kFlagTimeout);
+    } else if (warp == 9) {
+        // ================================================== MMA issue
+        constexpr uint32_t kIdS = mma_idesc(128, 128, !FP8, false);
+        constexpr uint32_t kIdO = mma_idesc(128, 128, !FP8, true);
+        const uint32_t leader = elect_one();
+        int units = 0, steps = 0, slot = 0;
+        uint32_t phase = 0, fixed_phase = 0;
+        uint32_t counts = 0;        // parities of the tiles' P (bits 0, 8) and O (bits 4, 12)
+        bool ok = true;
+        // S columns <- Q tile i . K box in slot s, elements 128 * half ...
+        const auto qk = [&](uint32_t d, int i, int s, int half) {
+            const uint32_t a = smem + i * C::QTILE + half * kBox, b = ring + s * kBox;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t off = (kk >> 2) * kLine + (kk & 3) * 32;
+                mma_ss(leader, tmem + d, smem_desc(a + off, 16, 1024),
+                       smem_desc(b + off, 16, 1024), kIdS, half > 0 || kk > 0);
+            }
+        };
+        // O columns (+)= P (in S columns c) . V box in slot s, one half of the keys
+        const auto pv = [&](uint32_t d, uint32_t c, int s, int half, bool acc) {
+            const uint32_t b = ring + s * kBox;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_ts(leader, tmem + d, tmem + c + (4 * half + kk) * 8,
+                       smem_desc(b + (4 * half + kk) * 2048, kLine, 1024), kIdO,
+                       acc || half > 0 || kk > 0);
+        };
+        // the ring's next box; its slot is returned, -1 after a timeout
+        const auto next_box = [&](bool fix) {
+            const int s = slot;
+            bool got;
+            if (fix && !FP8) {
+                got = wait(meta.fixed[s], (fixed_phase >> s) & 1);
+                fixed_phase ^= 1u << s;
+            } else {
+                got = wait(meta.full[s], phase);
+            }
+            if (++slot == C::NS) {
+                slot = 0;
+                phase ^= 1;
+            }
+            return got ? s : -1;
+        };
+        while (ok && next_piece()) {
+            const UnitKeys<NQ> k = unit_keys<NQ>(p, u, tpq);
+            if (k.kb >= k.ke) continue;
+            if (!(ok = wait(FP8 ? meta.q_ready : meta.q_full, units & 1))) break;
+            ++units;
+            if (NQ == 2) {
+                int sk = next_box(false);
+                ok = sk >= 0;
+                if (!ok) break;
+                tcgen05_fence_after();
+#pragma unroll
+                for (int i = 0; i < NQ; ++i)
+                    if (k.active(i, k.kb)) {
+                        qk(i * 128, i, sk, 0);
+                        mma_commit(leader, bar(meta.s_ready[i]));
+                    }
+                mma_commit(leader, bar(meta.empty[sk]));
+                if (k.kb + 1 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                for (int j = k.kb; j < k.ke; ++j) {
+                    const bool more = j + 1 < k.ke;
+                    const int sv = next_box(k.partial(j));
+                    ok = sv >= 0;
+                    if (ok && more) {
+                        sk = next_box(false);
+                        ok = sk >= 0;
+                    }
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int i = 0; i < NQ; ++i) {
+                        const int kb = i ? k.t[NQ - 1].kb : k.t[0].kb;
+                        const int ke = i ? k.t[NQ - 1].ke : k.t[0].ke;
+                        if (j >= kb && j < ke) {
+                            const uint32_t n = counts >> (8 * i);      // S tiles so far, O tiles so far
+                            if (j == kb) ok = wait(meta.o_free[i], ((n >> 4) & 1) ^ 1);
+#pragma unroll 1
+                            for (int h = 0; h < 2; ++h) {
+                                ok = ok && wait(meta.p_ready[i][h], n & 1);
+                                if (!ok) break;
+                                tcgen05_fence_after();
+                                pv(kOCol + i * 128, i * 128, sv, h, j > kb);
+                            }
+                            if (!ok) break;
+                            counts ^= 1u << (8 * i);
+                            if (j + 1 == ke) {
+                                mma_commit(leader, bar(meta.o_done[i]));
+                                counts ^= 16u << (8 * i);
+                            }
+                        }
+                        if (i == NQ - 1) mma_commit(leader, bar(meta.empty[sv]));
+                        if (j + 1 >= kb && j + 1 < ke) {
+                            qk(i * 128, i, sk, 0);
+                            mma_commit(leader, bar(meta.s_ready[i]));
+                        }
+                    }
+                    if (!ok) break;
+                    if (more) {
+                        mma_commit(leader, bar(meta.empty[sk]));
+                        if (j + 2 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                    }
+                }
+            } else {
+                const auto qk_tile = [&](int step) {
+                    for (int b = 0; b < C::BOXES; ++b) {
+                        const int s = next_box(false);
+                        if (s < 0) return false;
+                        tcgen05_fence_after();
+                        qk((step & 1) * 128, 0, s, b);
+                        mma_commit(leader, bar(meta.empty[s]));
+                    }
+                    mma_commit(leader, bar(meta.s_ready[step & 1]));
+                    return true;
+                };
+                ok = qk_tile(steps);
+                if (ok && k.kb + 1 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                for (int j = k.kb; ok && j < k.ke; ++j, ++steps) {
+                    if (j + 1 < k.ke) {
+                        if (!(ok = qk_tile(steps + 1))) break;
+                        if (j + 2 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                    }
+                    if (j == k.kb) ok = wait(meta.o_free[0], ((counts >> 4) & 1) ^ 1);
+#pragma unroll 1
+                    for (int b = 0; b < C::BOXES; ++b) {
+                        const int s = next_box(k.partial(j));
+                        ok = ok && s >= 0;
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            if (b == 0)
+                                ok = ok && wait(meta.p_ready[steps & 1][h], (steps >> 1) & 1);
+                            if (!ok) break;
+                            tcgen05_fence_after();
+                            pv(kOCol + b * 128, (steps & 1) * 128, s, h, j > k.kb);
+                        }
+                        if (!ok) break;
+                        mma_commit(leader, bar(meta.empty[s]));
+                    }
+                    if (!ok) break;
+                    mma_commit(leader, bar(meta.pv_done));
+                    if (j + 1 == k.ke) mma_commit(leader, bar(meta.o_done[0]));
+                }
+                counts ^= 16;
+            }
+        }
+        // the tensor cores must be done with shared and tensor memory
+        mma_commit(leader, bar(meta.drain));
+        if (!mbar_wait_bounded(bar(meta.drain), 0, kDrainWaitNs)) raise_flag(p.flags, kFlagTimeout);
+        __syncwarp();
+    } else if (warp >= 10) {
+        // ================================================== V warps
+        const int tid = threadIdx.x - 320;
+        int box = 0, units = 0;
+        bool ok = true;
+        while (ok && next_piece()) {
+            const UnitKeys<NQ> k = unit_keys<NQ>(p, u, tpq);
+            if (k.kb >= k.ke) continue;
+            if (FP8) {
+                if (!(ok = wait(meta.q_full, units & 1))) break;
+                for (int r = tid; r < NQ * 128; r += 64) {
+                    if (k.t[(r >> 7) % NQ].ntok > 0)
+                        row_mult[(units & 1) * 256 + r] =
+                            convert_q_row(smem + (r >> 7) * C::QTILE, r & 127);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(meta.q_ready));
+            }
+            ++units;
+            // one box: j its key tile, v whether it is of V
+            const auto take = [&](int j, bool v) {
+                const int s = box % C::NS;
+                const bool part = v && k.partial(j);
+                const int j0 = j * kKeys;
+                const int lo = part ? k.lo - j0 : 0, hi = part ? k.hi - j0 : kKeys;
+                bool bad = false;
+                if (FP8) {
+                    const int r = box % (FP8 ? C::NR : 1);
+                    if (!wait(meta.raw_full[r], (box / (FP8 ? C::NR : 1)) & 1)) return false;
+                    if (!wait(meta.empty[s], ((box / C::NS) & 1) ^ 1)) return false;
+                    bad = convert_box(raw_ring + r * kRawBox, ring + s * kBox, lo, hi, tid);
+                    fence_proxy_async();
+                    if (part && bad) meta.redo[units % kRedoSlots] = units;
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(meta.raw_empty[r]));
+                        mbar_arrive(bar(meta.full[s]));
+                    }
+                } else {
+                    if (!wait(meta.full[s], (box / C::NS) & 1)) return false;
+                    if (part) {
+                        bad = clean_box(ring + s * kBox, lo, hi, k.all_lo - j0, k.all_hi - j0, tid);
+                        fence_proxy_async();
+                        if (bad) meta.redo[units % kRedoSlots] = units;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(meta.fixed[s]));
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(meta.empty[s]));
+                }
+                ++box;
+                return true;
+            };
+            if (NQ == 2) {
+                for (int j = k.kb; ok && j < k.ke; ++j) ok = take(j, false) && take(j, true);
+            } else {
+                for (int b = 0; ok && b < C::BOXES; ++b) ok = take(k.kb, false);
+                for (int j = k.kb; ok && j < k.ke; ++j) {
+                    if (j + 1 < k.ke)
+                        for (int b = 0; ok && b < C::BOXES; ++b) ok = take(j + 1, false);
+                    for (int b = 0; ok && b < C::BOXES; ++b) ok = take(j, true);
+                }
+            }
+        }
+    }
+    } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if (NQ == 2 || warp < 4) {
+        // ================================================== softmax
+        const int t = NQ == 2 ? warp >> 2 : 0;
+        const int r = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // TMEM lane 32 * (warp & 3)
+        const int g = p.group;
+        const int tok = r / g, hd = r - tok * g;
+        const int tok_first = (r & ~31) / g, tok_last = (r | 31) / g;   // of the warp
+        constexpr float kLog2e = 1.4426950408889634f;
+        int units = 0, steps = 0, done = 0;
+        bool ok = true;
+        while (ok && next_piece()) {
+            const UnitKeys<NQ> k = unit_keys<NQ>(p, u, tpq);
+            if (k.kb < k.ke) ++units;
+            const TileKeys &tk = k.t[t];
+            if (tk.ntok <= 0) continue;
+            const bool valid = tok < tk.ntok;
+            const int hi = tk.p0 + tok + 1, lo = p.window > 0 ? hi - p.window : 0;
+            float m = -INFINITY, l = 0.f;
+            bool redo = false;
+            const bool any = tk.kb < tk.ke;
+            if (any) {
+                float mult = 0.f;
+                float2 l2 = make_float2(0.f, 0.f);
+                for (int j = tk.kb; j < tk.ke; ++j, ++steps) {
+                    const int sb = NQ == 2 ? t : steps & 1;
+                    if (!(ok = wait(meta.s_ready[sb], (NQ == 2 ? steps : steps >> 1) & 1))) break;
+                    tcgen05_fence_after();
+                    const uint32_t scol = tmem + lanes + sb * 128;
+                    if (j == tk.kb) {
+                        mult = p.scale * kLog2e;
+                        if (FP8) mult *= __ldg(p.k_scale + u.h) * row_mult[((units - 1) & 1) * 256 + t * 128 + r];
+                        // a scale of zero: every visible key weighs the same,
+                        // and masked scores (-inf) must still vanish
+                        if (mult == 0.f) mult = 0x1p-126f;
+                    }
+                    const bool masked = k.masked(t, j);
+                    if (masked || mult < 0.f) {
+                        // scores are changed where they lie: hidden ones to
+                        // -inf, and all of them negated for a negative scale;
+                        // columns [b, a) are the row's
+                        const int a = masked ? hi - j * kKeys : 128, b = masked ? lo - j * kKeys : 0;
+                        const int a0 = a + (masked ? tok_first - tok : 0);
+                        const int b1 = b + (masked ? tok_last - tok : 0);
+#pragma unroll 1
+                        for (int c = 0; c < 128; c += 32) {
+                            if (mult >= 0.f && a0 >= c + 32 && b1 <= c) continue;
+                            float s[32];
+                            tmem_ld32(scol + c, s);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                asm volatile("" : "+f"(s[i]));
+                                s[i] = mult < 0.f ? -s[i] : s[i];
+                                s[i] = i < a - c && i >= b - c ? s[i] : -INFINITY;
+                            }
+                            tmem_st32(scol + c, s);
+                        }
+                        tmem_wait_st();
+                    }
+                    float mx = -INFINITY;
+                    {
+                        float s[128];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld32(scol + c * 32, s + c * 32);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 128; ++c) asm volatile("" : "+f"(s[c]));
+                        float m4[4] = {mx, mx, mx, mx};
+#pragma unroll
+                        for (int c = 0; c < 128; c += 8)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                m4[i] = max3_nan(m4[i], s[c + i], s[c + 4 + i]);
+                        mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
+                    }
+                    const float am = fabsf(mult);
+                    const float top = valid ? mx * am : -INFINITY;
+                    // also for NaN, which poisons the row's sum, and +inf
+                    const bool move = !(top <= m + 8.f);
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float m_new = move ? top : m;
+                        float alpha = move ? ex2(m - m_new) : 1.f;
+                        m = m_new;
+                        if (!(top < INFINITY)) alpha = l2.x = NAN;
+                        l2 = mul2(l2, make_float2(alpha, alpha));
+                        if (j > tk.kb) {
+                            if (NQ == 1) {
+                                if (!(ok = wait(meta.pv_done, (steps - 1) & 1))) break;
+                                tcgen05_fence_after();
+                            }
+                            const uint32_t ocol = tmem + lanes + kOCol + t * 128;
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(ocol + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    asm volatile("" : "+r"(o[i]));
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                                }
+                                tmem_st16(ocol + c, o);
+                            }
+                        }
+                    }
+                    const float mu = m == -INFINITY ? 0.f : -m;
+                    const float2 k2 = make_float2(am, am), m2 = make_float2(mu, mu);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float s[32];
+                        uint32_t w[16];
+                        tmem_ld32(scol + c * 32, s);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(s[i]));
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float2 x = fma2(make_float2(s[i], s[i + 1]), k2, m2);
+                            if ((i / 2) % 8 >= 8 - kPolyOf8) {
+                                x = exp2_poly2(x);
+                            } else {
+                                x.x = ex2(x.x);
+                                x.y = ex2(x.y);
+                            }
+                            l2 = add2(l2, x);
+                            w[i / 2] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
+                        }
+                        tmem_st16(scol + c * 16, w);
+                        if (c & 1) {
+                            tmem_wait_st();
+                            tcgen05_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(meta.p_ready[sb][c >> 1]));
+                        }
+                    }
+                }
+                if (!ok) break;
+                l = l2.x + l2.y;
+                if (!(ok = wait(meta.o_done[t], done & 1))) break;
+                ++done;
+                tcgen05_fence_after();
+                redo = reinterpret_cast<volatile uint32_t *>(meta.redo)[units % kRedoSlots] ==
+                       static_cast<uint32_t>(units);
+            }
+            const float vs = FP8 ? __ldg(p.v_scale + u.h) : 1.f;
+            if (redo) {
+                if (lane == 0) mbar_arrive(bar(meta.o_free[t]));
+                KvRows kv;
+                kv.flags = p.flags;
+                kv.head = u.h; kv.hkv = p.num_kv_heads; kv.bs = p.block_size;
+                kv.num_blocks = p.num_blocks;
+                kv.row_bytes = FP8 ? D : 2 * D;
+                kv.table = p.block_table ? p.block_table + static_cast<int64_t>(u.seq) * p.max_blocks_per_seq
+                                         : nullptr;
+                kv.k_stride = p.k_stride * 2;
+                kv.v_stride = p.v_stride * 2;
+                const int64_t off = p.block_table ? 0 : static_cast<int64_t>(u.h) * D * 2;
+                kv.k = static_cast<const uint8_t *>(p.k) + off + (p.block_table ? 0 : u.kv0 * kv.k_stride);
+                kv.v = static_cast<const uint8_t *>(p.v) + off + (p.block_table ? 0 : u.kv0 * kv.v_stride);
+                const float sl2 = p.scale * kLog2e * (FP8 ? __ldg(p.k_scale + u.h) : 1.f);
+                for (int rr = 0; rr < 32; ++rr) {
+                    const int ro = __shfl_sync(0xffffffffu, r, rr);
+                    const int tk_i = ro / g, hd_i = ro - tk_i * g;
+                    if (tk_i >= tk.ntok) continue;
+                    const int h1 = tk.p0 + tk_i + 1;
+                    const int a = max(p.window > 0 ? max(0, h1 - p.window) : 0, tk.kb * kKeys);
+                    const int b = min(h1, tk.ke * kKeys);
+                    const int64_t tr = u.row0 + t * tpq + tk_i;
+                    const int q1 = u.h * g + hd_i;
+                    float acc[D / 32], mm, ll;
+                    attend_row<D, FP8>(p.q + tr * p.q_stride + q1 * D, kv, a, b, sl2, acc, mm, ll);
+                    const float inv = ll == 0.f ? 0.f : vs / ll;
+                    const int64_t orow = tr * p.num_q_heads + q1;
+                    if (u.slot >= 0) {
+                        const int64_t pr = (static_cast<int64_t>(u.slot) * NQ + t) * 128 + ro;
+                        for (int i = 0; i < D / 32; ++i)
+                            p.o_part[pr * D + lane * (D / 32) + i] = acc[i] * inv;
+                        if (lane == 0)
+                            p.lse_part[pr] = ll == 0.f ? -INFINITY : mm * 0.6931471805599453f + logf(ll);
+                    } else {
+                        uint32_t *o = reinterpret_cast<uint32_t *>(p.out + orow * D) + lane * (D / 64);
+                        for (int i = 0; i < D / 64; ++i)
+                            o[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+                        if (p.lse_out && lane == 0)
+                            p.lse_out[orow] = ll == 0.f ? -INFINITY : mm * 0.6931471805599453f + logf(ll);
+                    }
+                }
+                continue;
+            }
+            const bool dead = l == 0.f;
+            const float inv = dead ? 0.f : vs / l;
+            const float lse = dead ? -INFINITY : m * 0.6931471805599453f + logf(l);
+            // Rows leave through shared memory, 128 bytes of the warp's 32 rows
+            // at a time, so that eight lanes write one row's 128 bytes (a row
+            // per lane took 32 times the store passes).
+            const bool part = u.slot >= 0;
+            const int64_t row0 = part ? (static_cast<int64_t>(u.slot) * NQ + t) * 128
+                                      : static_cast<int64_t>(u.row0 + t * tpq) * p.num_q_heads + u.h * g;
+            const int rel = !valid ? -1 : part ? r : tok * p.num_q_heads + hd;
+            const uint32_t stage = smem + C::OFF_STAGE + (t * 4 + (warp & 3)) * 4096;
+            const auto put = [&](int ch, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+                sts128(stage + lane * 128 + ((ch ^ (lane & 7)) << 4), x, y, z, w);
+            };
+            const auto flush = [&](uint8_t *base, int64_t row_bytes) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int rr = i * 4 + (lane >> 3), ch = lane & 7;
+                    const int to = __shfl_sync(0xffffffffu, rel, rr);
+                    uint4 x;
+                    lds128(stage + rr * 128 + ((ch ^ (rr & 7)) << 4), x.x, x.y, x.z, x.w);
+                    if (to >= 0) *reinterpret_cast<uint4 *>(base + to * row_bytes + ch * 16) = x;
+                }
+                __syncwarp();
+            };
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                if (any) {
+                    tmem_ld32(tmem + lanes + kOCol + t * 128 + c, o);
+                    tmem_wait_ld();
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(o[i]));
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = dead ? 0.f : o[i] * inv;
+                if (part) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        put(i, __float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                            __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
+                    flush(reinterpret_cast<uint8_t *>(p.o_part + row0 * D + c), D * 4);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        put((c & 32) / 8 + i, pack_bf16x2(o[8 * i], o[8 * i + 1]),
+                            pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                            pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                            pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+                    if (c & 32) flush(reinterpret_cast<uint8_t *>(p.out + row0 * D + c - 32), D * 2);
+                }
+            }
+            if (any) {
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(meta.o_free[t]));
+            }
+            if (valid) {
+                if (part) p.lse_part[row0 + r] = lse;
+                else if (p.lse_out) p.lse_out[row0 + rel] = lse;
+            }
+        }
+    }
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tcgen05_fence_after();
+        tmem_dealloc(*reinterpret_cast<volatile uint32_t *>(&meta.tmem), 512);
+    }
+}
+
+}  // namespace pgd

@@ -56,6 +56,8 @@ namespace pgd {
 constexpr uint32_t kLine = 128 * 128;         // bytes of a line: 128 rows x 128 B
 constexpr uint32_t kBox = 2 * kLine;          // [128 keys][128 dims], 16-bit
 constexpr uint32_t kRawBox = kLine;           // [128 keys][128 dims], 8-bit
+// Of every 8 pairs of exponentials, how many are computed with FMAs.
+constexpr int kPolyOf8 = 2;
 constexpr int kRedoSlots = 8;
 constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;   // 8 warps and 4: 12 x 168 in all
 constexpr uint32_t kMetaBytes = 1024;
@@ -66,20 +68,23 @@ struct PrefillCfg {
     static constexpr int LINES = D / 64;              // lines of a Q tile
     static constexpr int BOXES = D / 128;             // boxes of a K or V tile
     static constexpr uint32_t QTILE = LINES * kLine;
-    static constexpr int NS = FP8 ? 3 : 5;            // ring of 16-bit boxes
-    static constexpr int NR = FP8 ? 3 : 0;            // ring of raw E4M3 boxes
+    static constexpr int NS = FP8 ? 3 : 4;            // ring of 16-bit boxes
+    static constexpr int NR = FP8 ? 2 : 0;            // ring of raw E4M3 boxes
+    static constexpr uint32_t STAGE = NQ * 4 * 4096;  // outputs on their way out, 4 KB a warp
     static constexpr uint32_t OFF_RING = NQ * QTILE;
     static constexpr uint32_t OFF_RAW = OFF_RING + NS * kBox;
-    static constexpr uint32_t OFF_META = OFF_RAW + NR * kRawBox;
-    static constexpr uint32_t SMEM = OFF_META + kMetaBytes + (FP8 ? 2048 : 0) + 1024;   // + alignment
+    static constexpr uint32_t OFF_STAGE = OFF_RAW + NR * kRawBox;
+    static constexpr uint32_t OFF_META = OFF_STAGE + STAGE;
+    static constexpr uint32_t SMEM = OFF_META + kMetaBytes + (FP8 ? 2048 : 0);
+    static_assert(SMEM <= 232448, "more shared memory than a CTA has");
 };
 
 // Barriers and small state behind the tiles (for FP8, 2 x 256 multipliers of
 // the query rows follow).
 struct PrefillMeta {
     uint64_t q_full, q_ready, q_empty, drain, pv_done;
-    uint64_t s_ready[2], p_ready[2], o_done[2], o_free[2];
-    uint64_t full[5], empty[5], fixed[5];
+    uint64_t s_ready[2], p_ready[2][2], o_done[2], o_free[2];
+    uint64_t full[4], empty[4], fixed[4];
     uint64_t raw_full[3], raw_empty[3];
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     Piece piece[kPieces];
@@ -96,29 +101,27 @@ struct PrefillMaps {
 struct TileKeys {
     int ntok;           // query tokens of the tile
     int p0;             // position of the first
-    int lo, hi;         // visible positions of all its rows together
-    int kb, ke;         // key tiles of this split
-    int wlo;            // keys below this are hidden from the last row
+    int kb, ke;         // key tiles of this piece
+    int mlo, mhi;       // tiles below mlo or from mhi on are not seen whole by every row
 };
 
 template <int NQ>
 struct UnitKeys {
     TileKeys t[NQ];
-    int kb, ke, lo, hi;
+    int kb, ke;
+    int lo, hi;         // positions that some row sees (whole unit)
+    int all_lo, all_hi; // positions that every row sees
+    int part_lo, part_hi;
 
     __device__ __forceinline__ bool active(int i, int j) const {
         return j >= t[i].kb && j < t[i].ke;
     }
     // whether some row of query tile i does not see all of key tile j
     __device__ __forceinline__ bool masked(int i, int j) const {
-        return (j + 1) * kKeys > t[i].p0 + 1 || j * kKeys < t[i].wlo;
+        return j < t[i].mlo || j >= t[i].mhi;
     }
-    __device__ __forceinline__ bool partial(int j) const {
-        bool p = false;
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) p |= active(i, j) && masked(i, j);
-        return p;
-    }
+    // the same for the unit's active tiles (their ranges leave no gap)
+    __device__ __forceinline__ bool partial(int j) const { return j < part_lo || j >= part_hi; }
 };
 
 template <int NQ>
@@ -126,42 +129,53 @@ __device__ __forceinline__ UnitKeys<NQ> unit_keys(const PrefillParams &p, const 
     UnitKeys<NQ> k;
     k.kb = u.kb;
     k.ke = u.ke;
-    k.lo = 0x7fffffff;
-    k.hi = 0;
+    k.hi = u.pos0 + u.ntok;
+    k.lo = p.window > 0 ? max(0, u.pos0 + 1 - p.window) : 0;
+    k.all_hi = u.pos0 + 1;
+    k.all_lo = p.window > 0 ? k.hi - p.window : 0;
+    k.part_lo = 0;
+    k.part_hi = 0x7fffffff;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
         TileKeys &t = k.t[i];
         t.ntok = min(tpq, u.ntok - i * tpq);
         t.p0 = u.pos0 + i * tpq;
-        t.hi = t.ntok > 0 ? t.p0 + t.ntok : 0;
-        t.lo = p.window > 0 ? max(0, t.p0 + 1 - p.window) : 0;
-        t.wlo = p.window > 0 ? t.p0 + t.ntok - p.window : 0;
-        t.kb = t.ke = 0;
-        if (t.hi > 0) {
-            t.kb = max(t.lo / kKeys, u.kb);
-            t.ke = max(t.kb, min((t.hi + kKeys - 1) / kKeys, u.ke));
-            k.lo = min(k.lo, t.lo);
-            k.hi = max(k.hi, t.hi);
+        t.kb = t.ke = t.mlo = t.mhi = 0;
+        const int hi = t.p0 + t.ntok;
+        if (t.ntok > 0 && hi > 0) {
+            t.kb = max(p.window > 0 ? max(0, t.p0 + 1 - p.window) / kKeys : 0, u.kb);
+            t.ke = max(t.kb, min((hi + kKeys - 1) / kKeys, u.ke));
+            t.mlo = p.window > 0 ? (max(0, hi - p.window) + kKeys - 1) / kKeys : 0;
+            t.mhi = max(0, t.p0 + 1) / kKeys;
+            k.part_lo = max(k.part_lo, t.mlo);
+            k.part_hi = min(k.part_hi, t.mhi);
         }
     }
     return k;
 }
 
 // ---------------------------------------------------------------- the V warps
-// Zero the rows of a 16-bit V box that lie outside [lo, hi) of the tile's
-// keys, and tell whether any other holds a non-finite value.  64 threads.
-__device__ __forceinline__ bool clean_box(uint32_t box, int lo, int hi, int tid) {
+// Keep masked keys out of a 16-bit V box: zero the rows outside [lo, hi) of
+// the tile's keys, and tell whether one that only some query rows see, outside
+// [all_lo, all_hi), holds a non-finite value.  64 threads, 8 of them on one
+// row's 128-byte line.
+__device__ __forceinline__ bool clean_box(uint32_t box, int lo, int hi, int all_lo, int all_hi,
+                                          int tid) {
     bool bad = false;
-    for (int i = tid; i < 2 * 128 * 8; i += 64) {
-        const int r = (i >> 3) & 127;
-        const uint32_t a = box + (i >> 10) * kLine + r * 128 + (i & 7) * 16;
+    const uint32_t at = box + (tid & 7) * 16;
+    const int r0 = tid >> 3;
+    for (int r = r0; r < 128; r += 8) {
+        if (r >= all_lo && r < all_hi) continue;
+        const uint32_t a = at + r * 128;
         if (r < lo || r >= hi) {
             sts128(a, 0, 0, 0, 0);
+            sts128(a + kLine, 0, 0, 0, 0);
         } else {
-            uint32_t x[4];
+            uint32_t x[8];
             lds128(a, x[0], x[1], x[2], x[3]);
+            lds128(a + kLine, x[4], x[5], x[6], x[7]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 8; ++k)
                 bad |= (((x[k] & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u) != 0;
         }
     }
@@ -236,15 +250,67 @@ __device__ __forceinline__ float convert_q_row(uint32_t tile, int r) {
     return __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
 }
 
+// ---------------------------------------------------------------- softmax
+// max(a, b, c), NaN if one is
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// 2^x of a pair (x <= 9, or NaN, whose result is any number: the row's sum is
+// NaN already).  x = n + f with n the nearest integer, read off the low bits
+// of x + 1.5 * 2^23; 2^f on [-1/2, 1/2] by the polynomial of degree 5 with
+// constant term 1 and the least largest relative error (fitted by linear
+// programming; 2^-22.5 with its fp32 roundings), n added to the exponent.  At
+// the clamp, x = -127, f is 0 and the sum of the bits is 0 exactly: what a
+// mask set to -infinity weighs nothing.
+__device__ __forceinline__ float2 exp2_poly2(float2 x) {
+    const float2 magic = make_float2(12582912.f, 12582912.f), back = make_float2(-12582912.f, -12582912.f);
+    x.x = fmaxf(x.x, -127.f);
+    x.y = fmaxf(x.y, -127.f);
+    const float2 n = add2(x, magic);
+    const float2 f = fma2(add2(n, back), make_float2(-1.f, -1.f), x);
+    float2 q = make_float2(0.001326472731307149f, 0.001326472731307149f);
+    q = fma2(q, f, make_float2(0.009671512991189957f, 0.009671512991189957f));
+    q = fma2(q, f, make_float2(0.05550733581185341f, 0.05550733581185341f));
+    q = fma2(q, f, make_float2(0.24022242426872253f, 0.24022242426872253f));
+    q = fma2(q, f, make_float2(0.6931470036506653f, 0.6931470036506653f));
+    q = fma2(q, f, make_float2(1.f, 1.f));
+    return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(n.x) << 23)),
+                       __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(n.y) << 23)));
+}
+
 // ---------------------------------------------------------------- the kernel
+// A warp's wait for a phase, all lanes or none: false when `limit_ns` ran out
+// (the timeout flag is raised).  One short loop: the kernel's loops run from
+// the small instruction caches, and there are many waits.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                          uint32_t *flags) {
+    const uint32_t nap = limit_ns < 20000 ? static_cast<uint32_t>(limit_ns) : 20000u;
+    uint64_t t0 = 0;
+    while (!__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, nap))) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, now - t0 > limit_ns)) {
+            raise_flag(flags, kFlagTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kPrefillThreads, 1)
 prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) {
     using C = PrefillCfg<D, FP8>;
     constexpr int NQ = C::NQ;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t smem = (smem_u32(smem_raw) + 1023) & ~1023u;
-    uint8_t *smem_al = smem_raw + (smem - smem_u32(smem_raw));
+    extern __shared__ __align__(1024) uint8_t smem_al[];
+    const uint32_t smem = smem_u32(smem_al);
+    if (smem & 1023) {                           // the swizzled boxes start on 1024 bytes
+        if (threadIdx.x == 0) raise_flag(p.flags, kFlagTimeout);
+        return;
+    }
     PrefillMeta &meta = *reinterpret_cast<PrefillMeta *>(smem_al + C::OFF_META);
     float *row_mult = reinterpret_cast<float *>(smem_al + C::OFF_META + kMetaBytes);
     const uint32_t ring = smem + C::OFF_RING, raw_ring = smem + C::OFF_RAW;
@@ -259,11 +325,12 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         mbar_init(bar(meta.pv_done), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(meta.s_ready[i]), 1);
-            mbar_init(bar(meta.p_ready[i]), 4);
+            mbar_init(bar(meta.p_ready[i][0]), 4);
+            mbar_init(bar(meta.p_ready[i][1]), 4);
             mbar_init(bar(meta.o_done[i]), 1);
             mbar_init(bar(meta.o_free[i]), 4);
         }
-        for (int i = 0; i < 5; ++i) {
+        for (int i = 0; i < 4; ++i) {
             // 16-bit ring: filled by TMA and read by the MMA and the V warps,
             // or (FP8) filled by the two V warps and read by the MMA
             mbar_init(bar(meta.full[i]), FP8 ? 2 : 1);
@@ -289,21 +356,15 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
     tcgen05_fence_before();
     __syncthreads();
     tcgen05_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&meta.tmem);
+    constexpr uint32_t tmem = 0;                 // all 512 columns start at the first
     constexpr uint32_t kOCol = 256;              // O_t at kOCol + t * 128
     const int tpq = 128 / p.group;
     const uint64_t limit = p.wait_ns;
     Piece u;
     int piece = 0;
 
-    // one thread's wait; the warp form agrees over its lanes
-    const auto wait1 = [&](uint64_t &b, uint32_t parity) {
-        if (mbar_wait_bounded(smem_u32(&b), parity, limit)) return true;
-        raise_flag(p.flags, kFlagTimeout);
-        return false;
-    };
     const auto wait = [&](uint64_t &b, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait1(b, parity)) != 0;
+        return warp_wait(smem_u32(&b), parity, limit, p.flags);
     };
     // the next piece handed out by the producer; false at the end
     const auto next_piece = [&]() {
@@ -428,144 +489,151 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         // ================================================== MMA issue
         constexpr uint32_t kIdS = mma_idesc(128, 128, !FP8, false);
         constexpr uint32_t kIdO = mma_idesc(128, 128, !FP8, true);
-        int box = 0, units = 0, steps = 0;
-        int sc[2] = {0, 0}, oc[2] = {0, 0};
-        uint32_t fixed_phase = 0;
+        const uint32_t leader = elect_one();
+        int units = 0, steps = 0, slot = 0;
+        uint32_t phase = 0, fixed_phase = 0;
+        uint32_t counts = 0;        // parities of the tiles' P (bits 0, 8) and O (bits 4, 12)
         bool ok = true;
-        // S columns <- Q tile i . K box s, elements 128 * half ...
+        // S columns <- Q tile i . K box in slot s, elements 128 * half ...
         const auto qk = [&](uint32_t d, int i, int s, int half) {
             const uint32_t a = smem + i * C::QTILE + half * kBox, b = ring + s * kBox;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 const uint32_t off = (kk >> 2) * kLine + (kk & 3) * 32;
-                mma_ss(tmem + d, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), kIdS,
-                       half > 0 || kk > 0);
+                mma_ss(leader, tmem + d, smem_desc(a + off, 16, 1024),
+                       smem_desc(b + off, 16, 1024), kIdS, half > 0 || kk > 0);
             }
         };
-        // O columns (+)= P (in S columns c) . V box s
-        const auto pv = [&](uint32_t d, uint32_t c, int s, bool acc) {
+        // O columns (+)= P (in S columns c) . V box in slot s, one half of the keys
+        const auto pv = [&](uint32_t d, uint32_t c, int s, int half, bool acc) {
             const uint32_t b = ring + s * kBox;
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-                mma_ts(tmem + d, tmem + c + kk * 8, smem_desc(b + kk * 2048, kLine, 1024), kIdO,
-                       acc || kk > 0);
+            for (int kk = 0; kk < 4; ++kk)
+                mma_ts(leader, tmem + d, tmem + c + (4 * half + kk) * 8,
+                       smem_desc(b + (4 * half + kk) * 2048, kLine, 1024), kIdO,
+                       acc || half > 0 || kk > 0);
         };
-        const auto wait_box = [&](int i, bool fix) {
-            const int s = i % C::NS;
+        // the ring's next box; its slot is returned, -1 after a timeout
+        const auto next_box = [&](bool fix) {
+            const int s = slot;
+            bool got;
             if (fix && !FP8) {
-                const uint32_t ph = (fixed_phase >> s) & 1;
+                got = wait(meta.fixed[s], (fixed_phase >> s) & 1);
                 fixed_phase ^= 1u << s;
-                return wait1(meta.fixed[s], ph);
+            } else {
+                got = wait(meta.full[s], phase);
             }
-            return wait1(meta.full[s], (i / C::NS) & 1);
+            if (++slot == C::NS) {
+                slot = 0;
+                phase ^= 1;
+            }
+            return got ? s : -1;
         };
-        while (next_piece()) {
+        while (ok && next_piece()) {
             const UnitKeys<NQ> k = unit_keys<NQ>(p, u, tpq);
             if (k.kb >= k.ke) continue;
-            if (lane == 0 && ok) {
-                ok = wait1(FP8 ? meta.q_ready : meta.q_full, units & 1);
-                if (NQ == 2) {
-                    if (ok) ok = wait_box(box, false);
-                    tcgen05_fence_after();
-                    if (ok) {
+            if (!(ok = wait(FP8 ? meta.q_ready : meta.q_full, units & 1))) break;
+            ++units;
+            if (NQ == 2) {
+                int sk = next_box(false);
+                ok = sk >= 0;
+                if (!ok) break;
+                tcgen05_fence_after();
 #pragma unroll
-                        for (int i = 0; i < NQ; ++i)
-                            if (k.active(i, k.kb)) {
-                                qk(i * 128, i, box % C::NS, 0);
-                                mma_commit(bar(meta.s_ready[i]));
-                            }
-                        mma_commit(bar(meta.empty[box % C::NS]));
-                        if (k.kb + 1 == k.ke) mma_commit(bar(meta.q_empty));
-                        ++box;
+                for (int i = 0; i < NQ; ++i)
+                    if (k.active(i, k.kb)) {
+                        qk(i * 128, i, sk, 0);
+                        mma_commit(leader, bar(meta.s_ready[i]));
                     }
-                    for (int j = k.kb; ok && j < k.ke; ++j) {
-                        const bool more = j + 1 < k.ke;
-                        const int sv = box % C::NS, sk = (box + 1) % C::NS;
-                        bool have_v = false, have_k = false;
-#pragma unroll
-                        for (int i = 0; i < NQ; ++i) {
-                            if (ok && k.active(i, j)) {
-                                const bool first = j == k.t[i].kb;
-                                if (!have_v) ok = wait_box(box, k.partial(j));
-                                have_v = true;
-                                if (ok && first) ok = wait1(meta.o_free[i], (oc[i] & 1) ^ 1);
-                                if (ok) ok = wait1(meta.p_ready[i], sc[i] & 1);
-                                ++sc[i];
+                mma_commit(leader, bar(meta.empty[sk]));
+                if (k.kb + 1 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                for (int j = k.kb; j < k.ke; ++j) {
+                    const bool more = j + 1 < k.ke;
+                    const int sv = next_box(k.partial(j));
+                    ok = sv >= 0;
+                    if (ok && more) {
+                        sk = next_box(false);
+                        ok = sk >= 0;
+                    }
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int i = 0; i < NQ; ++i) {
+                        const int kb = i ? k.t[NQ - 1].kb : k.t[0].kb;
+                        const int ke = i ? k.t[NQ - 1].ke : k.t[0].ke;
+                        if (j >= kb && j < ke) {
+                            const uint32_t n = counts >> (8 * i);      // S tiles so far, O tiles so far
+                            if (j == kb) ok = wait(meta.o_free[i], ((n >> 4) & 1) ^ 1);
+#pragma unroll 1
+                            for (int h = 0; h < 2; ++h) {
+                                ok = ok && wait(meta.p_ready[i][h], n & 1);
+                                if (!ok) break;
                                 tcgen05_fence_after();
-                                if (ok) {
-                                    pv(kOCol + i * 128, i * 128, sv, !first);
-                                    if (j + 1 == k.t[i].ke) {
-                                        mma_commit(bar(meta.o_done[i]));
-                                        ++oc[i];
-                                    }
-                                }
+                                pv(kOCol + i * 128, i * 128, sv, h, j > kb);
                             }
-                            if (ok && more && k.active(i, j + 1)) {
-                                if (!have_k) ok = wait_box(box + 1, false);
-                                have_k = true;
-                                if (ok) {
-                                    tcgen05_fence_after();
-                                    qk(i * 128, i, sk, 0);
-                                    mma_commit(bar(meta.s_ready[i]));
-                                }
+                            if (!ok) break;
+                            counts ^= 1u << (8 * i);
+                            if (j + 1 == ke) {
+                                mma_commit(leader, bar(meta.o_done[i]));
+                                counts ^= 16u << (8 * i);
                             }
                         }
-                        if (ok) {
-                            mma_commit(bar(meta.empty[sv]));
-                            if (more) {
-                                mma_commit(bar(meta.empty[sk]));
-                                if (j + 2 == k.ke) mma_commit(bar(meta.q_empty));
-                            }
-                        }
-                        box += more ? 2 : 1;
-                    }
-                } else {
-                    const auto qk_tile = [&](int step) {
-                        for (int b = 0; b < C::BOXES; ++b) {
-                            if (!wait_box(box, false)) return false;
-                            tcgen05_fence_after();
-                            qk((step & 1) * 128, 0, box % C::NS, b);
-                            mma_commit(bar(meta.empty[box % C::NS]));
-                            ++box;
-                        }
-                        mma_commit(bar(meta.s_ready[step & 1]));
-                        return true;
-                    };
-                    if (ok) ok = qk_tile(steps);
-                    if (ok && k.kb + 1 == k.ke) mma_commit(bar(meta.q_empty));
-                    for (int j = k.kb; ok && j < k.ke; ++j, ++steps) {
-                        if (j + 1 < k.ke) {
-                            ok = qk_tile(steps + 1);
-                            if (ok && j + 2 == k.ke) mma_commit(bar(meta.q_empty));
-                        }
-                        if (ok && j == k.kb) ok = wait1(meta.o_free[0], (oc[0] & 1) ^ 1);
-                        if (ok) ok = wait1(meta.p_ready[steps & 1], (steps >> 1) & 1);
-                        for (int b = 0; ok && b < C::BOXES; ++b) {
-                            ok = wait_box(box, k.partial(j));
-                            tcgen05_fence_after();
-                            if (ok) {
-                                pv(kOCol + b * 128, (steps & 1) * 128, box % C::NS, j > k.kb);
-                                mma_commit(bar(meta.empty[box % C::NS]));
-                            }
-                            ++box;
-                        }
-                        if (ok) {
-                            mma_commit(bar(meta.pv_done));
-                            if (j + 1 == k.ke) mma_commit(bar(meta.o_done[0]));
+                        if (i == NQ - 1) mma_commit(leader, bar(meta.empty[sv]));
+                        if (j + 1 >= kb && j + 1 < ke) {
+                            qk(i * 128, i, sk, 0);
+                            mma_commit(leader, bar(meta.s_ready[i]));
                         }
                     }
-                    ++oc[0];
+                    if (!ok) break;
+                    if (more) {
+                        mma_commit(leader, bar(meta.empty[sk]));
+                        if (j + 2 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                    }
                 }
-                ++units;
+            } else {
+                const auto qk_tile = [&](int step) {
+                    for (int b = 0; b < C::BOXES; ++b) {
+                        const int s = next_box(false);
+                        if (s < 0) return false;
+                        tcgen05_fence_after();
+                        qk((step & 1) * 128, 0, s, b);
+                        mma_commit(leader, bar(meta.empty[s]));
+                    }
+                    mma_commit(leader, bar(meta.s_ready[step & 1]));
+                    return true;
+                };
+                ok = qk_tile(steps);
+                if (ok && k.kb + 1 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                for (int j = k.kb; ok && j < k.ke; ++j, ++steps) {
+                    if (j + 1 < k.ke) {
+                        if (!(ok = qk_tile(steps + 1))) break;
+                        if (j + 2 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                    }
+                    if (j == k.kb) ok = wait(meta.o_free[0], ((counts >> 4) & 1) ^ 1);
+#pragma unroll 1
+                    for (int b = 0; b < C::BOXES; ++b) {
+                        const int s = next_box(k.partial(j));
+                        ok = ok && s >= 0;
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            if (b == 0)
+                                ok = ok && wait(meta.p_ready[steps & 1][h], (steps >> 1) & 1);
+                            if (!ok) break;
+                            tcgen05_fence_after();
+                            pv(kOCol + b * 128, (steps & 1) * 128, s, h, j > k.kb);
+                        }
+                        if (!ok) break;
+                        mma_commit(leader, bar(meta.empty[s]));
+                    }
+                    if (!ok) break;
+                    mma_commit(leader, bar(meta.pv_done));
+                    if (j + 1 == k.ke) mma_commit(leader, bar(meta.o_done[0]));
+                }
+                counts ^= 16;
             }
-            if (!__shfl_sync(0xffffffffu, static_cast<int>(ok), 0)) break;
         }
         // the tensor cores must be done with shared and tensor memory
-        if (lane == 0) {
-            mma_commit(bar(meta.drain));
-            if (!mbar_wait_bounded(bar(meta.drain), 0, kDrainWaitNs))
-                raise_flag(p.flags, kFlagTimeout);
-        }
+        mma_commit(leader, bar(meta.drain));
+        if (!mbar_wait_bounded(bar(meta.drain), 0, kDrainWaitNs)) raise_flag(p.flags, kFlagTimeout);
         __syncwarp();
     } else if (warp >= 10) {
         // ================================================== V warps
@@ -591,7 +659,8 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             const auto take = [&](int j, bool v) {
                 const int s = box % C::NS;
                 const bool part = v && k.partial(j);
-                const int lo = part ? k.lo - j * kKeys : 0, hi = part ? k.hi - j * kKeys : kKeys;
+                const int j0 = j * kKeys;
+                const int lo = part ? k.lo - j0 : 0, hi = part ? k.hi - j0 : kKeys;
                 bool bad = false;
                 if (FP8) {
                     const int r = box % (FP8 ? C::NR : 1);
@@ -608,7 +677,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                 } else {
                     if (!wait(meta.full[s], (box / C::NS) & 1)) return false;
                     if (part) {
-                        bad = clean_box(ring + s * kBox, lo, hi, tid);
+                        bad = clean_box(ring + s * kBox, lo, hi, k.all_lo - j0, k.all_hi - j0, tid);
                         fence_proxy_async();
                         if (bad) meta.redo[units % kRedoSlots] = units;
                         __syncwarp();
@@ -650,23 +719,18 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             const TileKeys &tk = k.t[t];
             if (tk.ntok <= 0) continue;
             const bool valid = tok < tk.ntok;
-            const int hi = tk.p0 + tok + 1, lo = p.window > 0 ? hi - p.window : 0;
-            const int qh = u.h * g + hd;
-            const int64_t row = static_cast<int64_t>(u.row0 + t * tpq + tok) * p.num_q_heads + qh;
+            const int hi = tk.p0 + tok + 1;
             float m = -INFINITY, l = 0.f;
             bool redo = false;
             const bool any = tk.kb < tk.ke;
             if (any) {
                 float mult = 0.f;
                 float2 l2 = make_float2(0.f, 0.f);
-                for (int j = tk.kb; ok && j < tk.ke; ++j, ++steps) {
+                for (int j = tk.kb; j < tk.ke; ++j, ++steps) {
                     const int sb = NQ == 2 ? t : steps & 1;
                     if (!(ok = wait(meta.s_ready[sb], (NQ == 2 ? steps : steps >> 1) & 1))) break;
                     tcgen05_fence_after();
                     const uint32_t scol = tmem + lanes + sb * 128;
-                    float s[128];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(scol + c * 32, s + c * 32);
                     if (j == tk.kb) {
                         mult = p.scale * kLog2e;
                         if (FP8) mult *= __ldg(p.k_scale + u.h) * row_mult[((units - 1) & 1) * 256 + t * 128 + r];
@@ -674,35 +738,54 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                         // and masked scores (-inf) must still vanish
                         if (mult == 0.f) mult = 0x1p-126f;
                     }
-                    tmem_wait_ld();
+                    const bool masked = k.masked(t, j);
+                    if (__any_sync(0xffffffffu, masked || mult < 0.f)) {
+                        // scores are changed where they lie: hidden ones to
+                        // -inf, and all of them negated for a negative scale;
+                        // columns [b, a) are the row's
+                        const int a = masked ? hi - j * kKeys : kKeys;
+                        const int b = masked && p.window > 0 ? hi - p.window - j * kKeys : 0;
+#pragma unroll 1
+                        for (int c = 0; c < 128; c += 32) {
+                            if (!__any_sync(0xffffffffu, mult < 0.f || a < c + 32 || b > c)) continue;
+                            float s[32];
+                            tmem_ld32(scol + c, s);
+                            tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) asm volatile("" : "+f"(s[c]));
-                    if (k.masked(t, j)) {
-                        const int a = hi - j * kKeys, b = lo - j * kKeys;
-                        const float hide = mult < 0.f ? INFINITY : -INFINITY;
-#pragma unroll
-                        for (int c = 0; c < 128; ++c) s[c] = c < a && c >= b ? s[c] : hide;
+                            for (int i = 0; i < 32; ++i) {
+                                asm volatile("" : "+f"(s[i]));
+                                s[i] = mult < 0.f ? -s[i] : s[i];
+                                s[i] = c + i < a && c + i >= b ? s[i] : -INFINITY;
+                            }
+                            tmem_st32(scol + c, s);
+                        }
+                        tmem_wait_st();
                     }
-                    float mx;
-                    if (mult < 0.f) {
-                        mx = INFINITY;
+                    float mx = -INFINITY;
+                    {
+                        float s[128];
 #pragma unroll
-                        for (int c = 0; c < 128; ++c) mx = fminf(mx, s[c]);
-                    } else {
-                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        for (int c = 0; c < 4; ++c) tmem_ld32(scol + c * 32, s + c * 32);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 128; ++c) asm volatile("" : "+f"(s[c]));
+                        float m4[4] = {mx, mx, mx, mx};
 #pragma unroll
                         for (int c = 0; c < 128; c += 8)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                m4[i] = fmaxf(fmaxf(m4[i], s[c + 2 * i]), s[c + 2 * i + 1]);
-                        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                                m4[i] = max3_nan(m4[i], s[c + i], s[c + 4 + i]);
+                        mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
                     }
-                    const float top = valid ? mx * mult : -INFINITY;
-                    const bool move = top > m + 8.f;
+                    const float am = fabsf(mult);
+                    const float top = valid ? mx * am : -INFINITY;
+                    // also for NaN, which poisons the row's sum, and +inf
+                    const bool move = !(top <= m + 8.f);
                     if (__any_sync(0xffffffffu, move)) {
                         const float m_new = move ? top : m;
-                        const float alpha = move ? ex2(m - m_new) : 1.f;
+                        float alpha = move ? ex2(m - m_new) : 1.f;
                         m = m_new;
+                        if (!(top < INFINITY)) alpha = l2.x = NAN;
                         l2 = mul2(l2, make_float2(alpha, alpha));
                         if (j > tk.kb) {
                             if (NQ == 1) {
@@ -725,24 +808,35 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                         }
                     }
                     const float mu = m == -INFINITY ? 0.f : -m;
-                    const float2 k2 = make_float2(mult, mult), m2 = make_float2(mu, mu);
-#pragma unroll
-                    for (int c = 0; c < 128; c += 32) {
+                    const float2 k2 = make_float2(am, am), m2 = make_float2(mu, mu);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float s[32];
                         uint32_t w[16];
+                        tmem_ld32(scol + c * 32, s);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(s[i]));
 #pragma unroll
                         for (int i = 0; i < 32; i += 2) {
-                            float2 x = fma2(make_float2(s[c + i], s[c + i + 1]), k2, m2);
-                            x.x = ex2(x.x);
-                            x.y = ex2(x.y);
+                            float2 x = fma2(make_float2(s[i], s[i + 1]), k2, m2);
+                            if ((i / 2) % 8 >= 8 - kPolyOf8) {
+                                x = exp2_poly2(x);
+                            } else {
+                                x.x = ex2(x.x);
+                                x.y = ex2(x.y);
+                            }
                             l2 = add2(l2, x);
                             w[i / 2] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
                         }
-                        tmem_st16(scol + c / 2, w);
+                        tmem_st16(scol + c * 16, w);
+                        if (c & 1) {
+                            tmem_wait_st();
+                            tcgen05_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(meta.p_ready[sb][c >> 1]));
+                        }
                     }
-                    tmem_wait_st();
-                    tcgen05_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(meta.p_ready[sb]));
                 }
                 if (!ok) break;
                 l = l2.x + l2.y;
@@ -800,7 +894,29 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             const bool dead = l == 0.f;
             const float inv = dead ? 0.f : vs / l;
             const float lse = dead ? -INFINITY : m * 0.6931471805599453f + logf(l);
-            const int64_t prow = (static_cast<int64_t>(u.slot) * NQ + t) * 128 + r;
+            // Rows leave through shared memory, 128 bytes of the warp's 32 rows
+            // at a time, so that eight lanes write one row's 128 bytes (a row
+            // per lane took 32 times the store passes).
+            const bool part = u.slot >= 0;
+            const int64_t row0 = part ? (static_cast<int64_t>(u.slot) * NQ + t) * 128
+                                      : static_cast<int64_t>(u.row0 + t * tpq) * p.num_q_heads + u.h * g;
+            const int rel = !valid ? -1 : part ? r : tok * p.num_q_heads + hd;
+            const uint32_t stage = smem + C::OFF_STAGE + (t * 4 + (warp & 3)) * 4096;
+            const auto put = [&](int ch, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+                sts128(stage + lane * 128 + ((ch ^ (lane & 7)) << 4), x, y, z, w);
+            };
+            const auto flush = [&](uint8_t *base, int64_t row_bytes) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int rr = i * 4 + (lane >> 3), ch = lane & 7;
+                    const int to = __shfl_sync(0xffffffffu, rel, rr);
+                    uint4 x;
+                    lds128(stage + rr * 128 + ((ch ^ (rr & 7)) << 4), x.x, x.y, x.z, x.w);
+                    if (to >= 0) *reinterpret_cast<uint4 *>(base + to * row_bytes + ch * 16) = x;
+                }
+                __syncwarp();
+            };
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -812,20 +928,20 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                 for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(o[i]));
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = dead ? 0.f : o[i] * inv;
-                if (!valid) continue;
-                if (u.slot >= 0) {
-                    float4 *d = reinterpret_cast<float4 *>(p.o_part + prow * D + c);
+                if (part) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        d[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        put(i, __float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                            __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
+                    flush(reinterpret_cast<uint8_t *>(p.o_part + row0 * D + c), D * 4);
                 } else {
-                    uint4 *d = reinterpret_cast<uint4 *>(p.out + row * D + c);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        d[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]),
-                                          pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                                          pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
-                                          pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+                        put((c & 32) / 8 + i, pack_bf16x2(o[8 * i], o[8 * i + 1]),
+                            pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                            pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                            pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+                    if (c & 32) flush(reinterpret_cast<uint8_t *>(p.out + row0 * D + c - 32), D * 2);
                 }
             }
             if (any) {
@@ -834,8 +950,8 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                 if (lane == 0) mbar_arrive(bar(meta.o_free[t]));
             }
             if (valid) {
-                if (u.slot >= 0) p.lse_part[prow] = lse;
-                else if (p.lse_out) p.lse_out[row] = lse;
+                if (part) p.lse_part[row0 + r] = lse;
+                else if (p.lse_out) p.lse_out[row0 + rel] = lse;
             }
         }
     }
@@ -844,7 +960,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
     __syncthreads();
     if (warp == 9) {
         tcgen05_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(*reinterpret_cast<volatile uint32_t *>(&meta.tmem), 512);
     }
 }
 
