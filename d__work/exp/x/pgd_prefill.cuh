@@ -16,17 +16,20 @@
 // A unit that a boundary cuts leaves one unrounded piece per CTA in the
 // workspace; a second kernel merges them by log-sum-exp.
 //
-// CTA = 2 softmax warpgroups + one of four single warps:
+// CTA = 2 softmax warpgroups + 8 single warps:
 //   warps 0-3, 4-7   softmax; thread = query row (one TMEM lane)
 //   warp 8           finds the share, hands its pieces out, and loads: Q and
 //                    [128 keys x 128 dims] boxes of K and V into a ring (TMA)
-//   warp 9           issues the tcgen05.mma of S = Q K^T and O += P V
-//   warps 10, 11     keep masked keys out of V (below); for FP8 caches they
+//   warps 9, 10      issue the tcgen05.mma of S = Q K^T and O += P V, one
+//                    query tile each: an MMA of 64 cycles and a wait of about
+//                    100 alternate in one warp, which left the tensor cores
+//                    idle for 4 of 10 cycles
+//   warps 12 - 15    keep masked keys out of V (below); for FP8 caches they
 //                    also turn the E4M3 boxes and the query rows into f16
 // S, P and O live in tensor memory (512 columns):
-//   NQ = 2: S0 | S1 | O0 | O1, P_t in the columns of S_t.  The two tiles take
-//     turns: one's softmax runs while the other's products do, and S_t(j + 1)
-//     follows P_t(j) V(j) in issue order, so S_t ready means O_t is at rest.
+//   NQ = 2: S0 | S1 | O0 | O1, P_t in the columns of S_t.  One tile's softmax
+//     runs while the other's products do, and S_t(j + 1) follows P_t(j) V(j)
+//     in issue order, so S_t ready means O_t is at rest.
 //   NQ = 1: S0 | S1 | O (256): S(j + 1) is formed while softmax(j) runs.
 //
 // Softmax, one pass with a running reference m and sum l in fp32: the weights
@@ -59,7 +62,8 @@ constexpr uint32_t kRawBox = kLine;           // [128 keys][128 dims], 8-bit
 // Of every 8 pairs of exponentials, how many are computed with FMAs.
 constexpr int kPolyOf8 = 2;
 constexpr int kRedoSlots = 8;
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;   // 8 warps and 4: 12 x 168 in all
+constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;   // 8 warps each: 16 x 128 in all
+constexpr int kVWarps = 4;
 constexpr uint32_t kMetaBytes = 1024;
 
 template <int D, bool FP8>
@@ -157,14 +161,14 @@ __device__ __forceinline__ UnitKeys<NQ> unit_keys(const PrefillParams &p, const 
 // ---------------------------------------------------------------- the V warps
 // Keep masked keys out of a 16-bit V box: zero the rows outside [lo, hi) of
 // the tile's keys, and tell whether one that only some query rows see, outside
-// [all_lo, all_hi), holds a non-finite value.  64 threads, 8 of them on one
-// row's 128-byte line.
+// [all_lo, all_hi), holds a non-finite value.  8 threads on one row's 128-byte
+// line.
 __device__ __forceinline__ bool clean_box(uint32_t box, int lo, int hi, int all_lo, int all_hi,
                                           int tid) {
     bool bad = false;
     const uint32_t at = box + (tid & 7) * 16;
     const int r0 = tid >> 3;
-    for (int r = r0; r < 128; r += 8) {
+    for (int r = r0; r < 128; r += kVWarps * 4) {
         if (r >= all_lo && r < all_hi) continue;
         const uint32_t a = at + r * 128;
         if (r < lo || r >= hi) {
@@ -187,7 +191,7 @@ __device__ __forceinline__ bool clean_box(uint32_t box, int lo, int hi, int all_
 __device__ __forceinline__ bool convert_box(uint32_t raw, uint32_t box, int lo, int hi, int tid) {
     bool bad = false;
 #pragma unroll 4
-    for (int i = tid; i < 128 * 8; i += 64) {
+    for (int i = tid; i < 128 * 8; i += 32 * kVWarps) {
         const int r = i >> 3, c = i & 7, sw = r & 7;
         uint32_t x[4];
         lds128(raw + r * 128 + ((c ^ sw) << 4), x[0], x[1], x[2], x[3]);
@@ -287,6 +291,8 @@ __device__ __forceinline__ float2 exp2_poly2(float2 x) {
 // the small instruction caches, and there are many waits.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                           uint32_t *flags) {
+    if (__all_sync(0xffffffffu, limit_ns >= kDefaultWaitNs && mbar_try_wait(bar, parity)))
+        return true;                             // 50 cycles; with a time limit 100
     const uint32_t nap = limit_ns < 20000 ? static_cast<uint32_t>(limit_ns) : 20000u;
     uint64_t t0 = 0;
     while (!__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, nap))) {
@@ -319,9 +325,9 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
 
     if (threadIdx.x == 0) {
         mbar_init(bar(meta.q_full), 1);
-        mbar_init(bar(meta.q_ready), 2);
-        mbar_init(bar(meta.q_empty), 1);
-        mbar_init(bar(meta.drain), 1);
+        mbar_init(bar(meta.q_ready), kVWarps);
+        mbar_init(bar(meta.q_empty), NQ);
+        mbar_init(bar(meta.drain), NQ);
         mbar_init(bar(meta.pv_done), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(meta.s_ready[i]), 1);
@@ -332,18 +338,18 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         }
         for (int i = 0; i < 4; ++i) {
             // 16-bit ring: filled by TMA and read by the MMA and the V warps,
-            // or (FP8) filled by the two V warps and read by the MMA
-            mbar_init(bar(meta.full[i]), FP8 ? 2 : 1);
-            mbar_init(bar(meta.empty[i]), FP8 ? 1 : 3);
-            mbar_init(bar(meta.fixed[i]), 2);
+            // or (FP8) filled by the V warps and read by the MMA
+            mbar_init(bar(meta.full[i]), FP8 ? kVWarps : 1);
+            mbar_init(bar(meta.empty[i]), FP8 ? NQ : NQ + kVWarps);
+            mbar_init(bar(meta.fixed[i]), kVWarps);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(bar(meta.raw_full[i]), 1);
-            mbar_init(bar(meta.raw_empty[i]), 2);
+            mbar_init(bar(meta.raw_empty[i]), kVWarps);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(bar(meta.piece_full[i]), 1);
-            mbar_init(bar(meta.piece_empty[i]), 3 + 4 * NQ);   // MMA, V and softmax warps
+            mbar_init(bar(meta.piece_empty[i]), 5 * NQ + kVWarps);   // MMA, softmax, V warps
         }
         for (int i = 0; i < kRedoSlots; ++i) meta.redo[i] = 0;
         fence_mbar_init();
@@ -485,14 +491,15 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         if (units > 0)
             landed &= mbar_wait_bounded(bar(meta.q_full), (units - 1) & 1, kDrainWaitNs);
         if (!landed) raise_flag(p.flags, kFlagTimeout);
-    } else if (warp == 9) {
+    } else if (warp == 9 || (NQ == 2 && warp == 10)) {
         // ================================================== MMA issue
+        const int t = warp - 9;
         constexpr uint32_t kIdS = mma_idesc(128, 128, !FP8, false);
         constexpr uint32_t kIdO = mma_idesc(128, 128, !FP8, true);
         const uint32_t leader = elect_one();
         int units = 0, steps = 0, slot = 0;
         uint32_t phase = 0, fixed_phase = 0;
-        uint32_t counts = 0;        // parities of the tiles' P (bits 0, 8) and O (bits 4, 12)
+        int p_count = 0, o_count = 0;
         bool ok = true;
         // S columns <- Q tile i . K box in slot s, elements 128 * half ...
         const auto qk = [&](uint32_t d, int i, int s, int half) {
@@ -500,8 +507,8 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 const uint32_t off = (kk >> 2) * kLine + (kk & 3) * 32;
-                mma_ss(leader, tmem + d, smem_desc(a + off, 16, 1024),
-                       smem_desc(b + off, 16, 1024), kIdS, half > 0 || kk > 0);
+                mma_ss(tmem + d, desc_lo(a + off, 16), desc_lo(b + off, 16), kIdS,
+                       half > 0 || kk > 0);
             }
         };
         // O columns (+)= P (in S columns c) . V box in slot s, one half of the keys
@@ -509,25 +516,20 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             const uint32_t b = ring + s * kBox;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                mma_ts(leader, tmem + d, tmem + c + (4 * half + kk) * 8,
-                       smem_desc(b + (4 * half + kk) * 2048, kLine, 1024), kIdO,
-                       acc || half > 0 || kk > 0);
+                mma_ts(tmem + d, tmem + c + (4 * half + kk) * 8,
+                       desc_lo(b + (4 * half + kk) * 2048, kLine), kIdO, kk > 0 || acc);
         };
         // the ring's next box; its slot is returned, -1 after a timeout
         const auto next_box = [&](bool fix) {
             const int s = slot;
-            bool got;
-            if (fix && !FP8) {
-                got = wait(meta.fixed[s], (fixed_phase >> s) & 1);
-                fixed_phase ^= 1u << s;
-            } else {
-                got = wait(meta.full[s], phase);
-            }
+            const bool fixed = fix && !FP8;
+            const uint32_t parity = fixed ? (fixed_phase >> s) & 1 : phase;
+            if (fixed) fixed_phase ^= 1u << s;
             if (++slot == C::NS) {
                 slot = 0;
                 phase ^= 1;
             }
-            return got ? s : -1;
+            return wait(fixed ? meta.fixed[s] : meta.full[s], parity) ? s : -1;
         };
         while (ok && next_piece()) {
             const UnitKeys<NQ> k = unit_keys<NQ>(p, u, tpq);
@@ -535,58 +537,54 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             if (!(ok = wait(FP8 ? meta.q_ready : meta.q_full, units & 1))) break;
             ++units;
             if (NQ == 2) {
+                const int kb = t ? k.t[NQ - 1].kb : k.t[0].kb, ke = t ? k.t[NQ - 1].ke : k.t[0].ke;
+                // every box of the piece is waited for and released, used or not
                 int sk = next_box(false);
                 ok = sk >= 0;
                 if (!ok) break;
                 tcgen05_fence_after();
-#pragma unroll
-                for (int i = 0; i < NQ; ++i)
-                    if (k.active(i, k.kb)) {
-                        qk(i * 128, i, sk, 0);
-                        mma_commit(leader, bar(meta.s_ready[i]));
+                if (leader) {
+                    if (kb == k.kb && kb < ke) {
+                        qk(t * 128, t, sk, 0);
+                        mma_commit(bar(meta.s_ready[t]));
                     }
-                mma_commit(leader, bar(meta.empty[sk]));
-                if (k.kb + 1 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                    mma_commit(bar(meta.empty[sk]));
+                    if (k.kb + 1 == k.ke) mma_commit(bar(meta.q_empty));
+                }
                 for (int j = k.kb; j < k.ke; ++j) {
-                    const bool more = j + 1 < k.ke;
                     const int sv = next_box(k.partial(j));
                     ok = sv >= 0;
-                    if (ok && more) {
+                    if (j >= kb && j < ke) {
+                        if (j == kb) {
+                            ok = ok && wait(meta.o_free[t], (o_count & 1) ^ 1);
+                            ++o_count;
+                        }
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            ok = ok && wait(meta.p_ready[t][h], p_count & 1);
+                            if (!ok) break;
+                            tcgen05_fence_after();
+                            if (leader) pv(kOCol + t * 128, t * 128, sv, h, h > 0 || j > kb);
+                        }
+                        if (!ok) break;
+                        ++p_count;
+                        if (j + 1 == ke && leader) mma_commit(bar(meta.o_done[t]));
+                    }
+                    if (!ok) break;
+                    if (leader) mma_commit(bar(meta.empty[sv]));
+                    if (j + 1 < k.ke) {
                         sk = next_box(false);
                         ok = sk >= 0;
-                    }
-                    if (!ok) break;
-#pragma unroll 1
-                    for (int i = 0; i < NQ; ++i) {
-                        const int kb = i ? k.t[NQ - 1].kb : k.t[0].kb;
-                        const int ke = i ? k.t[NQ - 1].ke : k.t[0].ke;
-                        if (j >= kb && j < ke) {
-                            const uint32_t n = counts >> (8 * i);      // S tiles so far, O tiles so far
-                            if (j == kb) ok = wait(meta.o_free[i], ((n >> 4) & 1) ^ 1);
-#pragma unroll 1
-                            for (int h = 0; h < 2; ++h) {
-                                ok = ok && wait(meta.p_ready[i][h], n & 1);
-                                if (!ok) break;
-                                tcgen05_fence_after();
-                                pv(kOCol + i * 128, i * 128, sv, h, j > kb);
+                        if (!ok) break;
+                        tcgen05_fence_after();
+                        if (leader) {
+                            if (j + 1 >= kb && j + 1 < ke) {
+                                qk(t * 128, t, sk, 0);
+                                mma_commit(bar(meta.s_ready[t]));
                             }
-                            if (!ok) break;
-                            counts ^= 1u << (8 * i);
-                            if (j + 1 == ke) {
-                                mma_commit(leader, bar(meta.o_done[i]));
-                                counts ^= 16u << (8 * i);
-                            }
+                            mma_commit(bar(meta.empty[sk]));
+                            if (j + 2 == k.ke) mma_commit(bar(meta.q_empty));
                         }
-                        if (i == NQ - 1) mma_commit(leader, bar(meta.empty[sv]));
-                        if (j + 1 >= kb && j + 1 < ke) {
-                            qk(i * 128, i, sk, 0);
-                            mma_commit(leader, bar(meta.s_ready[i]));
-                        }
-                    }
-                    if (!ok) break;
-                    if (more) {
-                        mma_commit(leader, bar(meta.empty[sk]));
-                        if (j + 2 == k.ke) mma_commit(leader, bar(meta.q_empty));
                     }
                 }
             } else {
@@ -595,20 +593,22 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                         const int s = next_box(false);
                         if (s < 0) return false;
                         tcgen05_fence_after();
-                        qk((step & 1) * 128, 0, s, b);
-                        mma_commit(leader, bar(meta.empty[s]));
+                        if (leader) {
+                            qk((step & 1) * 128, 0, s, b);
+                            mma_commit(bar(meta.empty[s]));
+                            if (b == C::BOXES - 1) mma_commit(bar(meta.s_ready[step & 1]));
+                        }
                     }
-                    mma_commit(leader, bar(meta.s_ready[step & 1]));
                     return true;
                 };
                 ok = qk_tile(steps);
-                if (ok && k.kb + 1 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                if (ok && k.kb + 1 == k.ke && leader) mma_commit(bar(meta.q_empty));
                 for (int j = k.kb; ok && j < k.ke; ++j, ++steps) {
                     if (j + 1 < k.ke) {
                         if (!(ok = qk_tile(steps + 1))) break;
-                        if (j + 2 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                        if (j + 2 == k.ke && leader) mma_commit(bar(meta.q_empty));
                     }
-                    if (j == k.kb) ok = wait(meta.o_free[0], ((counts >> 4) & 1) ^ 1);
+                    if (j == k.kb) ok = wait(meta.o_free[0], (o_count & 1) ^ 1);
 #pragma unroll 1
                     for (int b = 0; b < C::BOXES; ++b) {
                         const int s = next_box(k.partial(j));
@@ -619,25 +619,25 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                                 ok = ok && wait(meta.p_ready[steps & 1][h], (steps >> 1) & 1);
                             if (!ok) break;
                             tcgen05_fence_after();
-                            pv(kOCol + b * 128, (steps & 1) * 128, s, h, j > k.kb);
+                            if (leader) pv(kOCol + b * 128, (steps & 1) * 128, s, h, h > 0 || j > k.kb);
                         }
                         if (!ok) break;
-                        mma_commit(leader, bar(meta.empty[s]));
+                        if (leader) mma_commit(bar(meta.empty[s]));
                     }
                     if (!ok) break;
-                    mma_commit(leader, bar(meta.pv_done));
-                    if (j + 1 == k.ke) mma_commit(leader, bar(meta.o_done[0]));
+                    if (leader) mma_commit(bar(meta.pv_done));
+                    if (j + 1 == k.ke && leader) mma_commit(bar(meta.o_done[0]));
                 }
-                counts ^= 16;
+                ++o_count;
             }
         }
         // the tensor cores must be done with shared and tensor memory
-        mma_commit(leader, bar(meta.drain));
+        if (leader) mma_commit(bar(meta.drain));
         if (!mbar_wait_bounded(bar(meta.drain), 0, kDrainWaitNs)) raise_flag(p.flags, kFlagTimeout);
         __syncwarp();
-    } else if (warp >= 10) {
+    } else if (warp >= 12) {
         // ================================================== V warps
-        const int tid = threadIdx.x - 320;
+        const int tid = threadIdx.x - 384;
         int box = 0, units = 0;
         bool ok = true;
         while (ok && next_piece()) {
@@ -645,7 +645,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             if (k.kb >= k.ke) continue;
             if (FP8) {
                 if (!(ok = wait(meta.q_full, units & 1))) break;
-                for (int r = tid; r < NQ * 128; r += 64) {
+                for (int r = tid; r < NQ * 128; r += 32 * kVWarps) {
                     if (k.t[(r >> 7) % NQ].ntok > 0)
                         row_mult[(units & 1) * 256 + r] =
                             convert_q_row(smem + (r >> 7) * C::QTILE, r & 127);
@@ -710,7 +710,6 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // TMEM lane 32 * (warp & 3)
         const int g = p.group;
         const int tok = r / g, hd = r - tok * g;
-        const int tok_first = (r & ~31) / g, tok_last = (r | 31) / g;   // of the warp
         constexpr float kLog2e = 1.4426950408889634f;
         int units = 0, steps = 0, done = 0;
         bool ok = true;
@@ -720,7 +719,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             const TileKeys &tk = k.t[t];
             if (tk.ntok <= 0) continue;
             const bool valid = tok < tk.ntok;
-            const int hi = tk.p0 + tok + 1, lo = p.window > 0 ? hi - p.window : 0;
+            const int hi = tk.p0 + tok + 1;
             float m = -INFINITY, l = 0.f;
             bool redo = false;
             const bool any = tk.kb < tk.ke;
@@ -740,16 +739,15 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                         if (mult == 0.f) mult = 0x1p-126f;
                     }
                     const bool masked = k.masked(t, j);
-                    if (masked || mult < 0.f) {
+                    if (__any_sync(0xffffffffu, masked || mult < 0.f)) {
                         // scores are changed where they lie: hidden ones to
                         // -inf, and all of them negated for a negative scale;
                         // columns [b, a) are the row's
-                        const int a = masked ? hi - j * kKeys : 128, b = masked ? lo - j * kKeys : 0;
-                        const int a0 = a + (masked ? tok_first - tok : 0);
-                        const int b1 = b + (masked ? tok_last - tok : 0);
+                        const int a = masked ? hi - j * kKeys : kKeys;
+                        const int b = masked && p.window > 0 ? hi - p.window - j * kKeys : 0;
 #pragma unroll 1
                         for (int c = 0; c < 128; c += 32) {
-                            if (mult >= 0.f && a0 >= c + 32 && b1 <= c) continue;
+                            if (!__any_sync(0xffffffffu, mult < 0.f || a < c + 32 || b > c)) continue;
                             float s[32];
                             tmem_ld32(scol + c, s);
                             tmem_wait_ld();
@@ -757,28 +755,28 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                             for (int i = 0; i < 32; ++i) {
                                 asm volatile("" : "+f"(s[i]));
                                 s[i] = mult < 0.f ? -s[i] : s[i];
-                                s[i] = i < a - c && i >= b - c ? s[i] : -INFINITY;
+                                s[i] = c + i < a && c + i >= b ? s[i] : -INFINITY;
                             }
                             tmem_st32(scol + c, s);
                         }
                         tmem_wait_st();
                     }
-                    float mx = -INFINITY;
-                    {
-                        float s[128];
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld32(scol + c * 32, s + c * 32);
+                    for (int c0 = 0; c0 < 128; c0 += 64) {
+                        float s[64];
+                        tmem_ld32(scol + c0, s);
+                        tmem_ld32(scol + c0 + 32, s + 32);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 128; ++c) asm volatile("" : "+f"(s[c]));
-                        float m4[4] = {mx, mx, mx, mx};
+                        for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(s[c]));
 #pragma unroll
-                        for (int c = 0; c < 128; c += 8)
+                        for (int c = 0; c < 64; c += 8)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 m4[i] = max3_nan(m4[i], s[c + i], s[c + 4 + i]);
-                        mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
                     }
+                    const float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
                     const float am = fabsf(mult);
                     const float top = valid ? mx * am : -INFINITY;
                     // also for NaN, which poisons the row's sum, and +inf

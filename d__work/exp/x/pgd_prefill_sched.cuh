@@ -20,7 +20,7 @@
 
 namespace pgd {
 
-constexpr int kPrefillThreads = 384;
+constexpr int kPrefillThreads = 512;
 constexpr int kKeys = 128;           // keys per tile
 constexpr int kUnitKeys = 128;       // a unit's fixed cost, in keys
 constexpr int kPieces = 4;           // pieces handed out ahead

@@ -99,11 +99,12 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity,
 //   MN-major operand (rows = K, contiguous = N): a line is 64 elements of N,
 //     lines are `line` bytes apart; 8-row groups of K are 1024 bytes apart, so
 //     16 of K are 2048 bytes further.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
-    return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) |
-           (static_cast<uint64_t>(lead >> 4) << 16) | (static_cast<uint64_t>(stride >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+// Only the low word depends on the address; the high word is the stride and
+// the layout.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+    return (addr >> 4) | (lead >> 4 << 16);      // shared addresses are below 2^18
 }
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
 
 // Instruction descriptor of kind::f16: fp32 accumulation, bf16 or f16
 // operands (both the same), B K-major or MN-major.
@@ -112,9 +113,8 @@ constexpr uint32_t mma_idesc(int m, int n, bool bf16, bool b_mn_major) {
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// The tensor-core instructions are issued by one lane, by predicate: the warp
-// stays converged, so descriptors and addresses stay in uniform registers.
-// (Issued inside a one-lane branch, an MMA cost its warp about 90 cycles.)
+// The warp that issues tensor-core instructions stays converged; one elected
+// lane issues them in batches.
 __device__ __forceinline__ uint32_t elect_one() {   // 1 in one lane of the warp
     uint32_t r;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
@@ -123,29 +123,30 @@ __device__ __forceinline__ uint32_t elect_one() {   // 1 in one lane of the warp
 }
 
 // D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b,
-                                       uint32_t idesc, bool accumulate) {
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)),
-                   "r"(leader) : "memory");
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       bool accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)),
+                   "n"(kDescHi) : "memory");
 }
 
 // D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b,
-                                       uint32_t idesc, bool accumulate) {
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)),
-                   "r"(leader) : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       bool accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                 "mov.b64 db, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)),
+                   "n"(kDescHi) : "memory");
 }
 
-// One arrival on `bar` when every tensor-core operation the leader issued
+// One arrival on `bar` when every tensor-core operation this thread issued
 // before has completed.
-__device__ __forceinline__ void mma_commit(uint32_t leader, uint32_t bar) {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
-                 ::"r"(bar), "r"(leader) : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 ::"r"(bar) : "memory");
 }
 
 // Generic-proxy writes to shared memory before async-proxy (tensor core) reads.

@@ -316,7 +316,7 @@ pgd_status pgd_paged_decode_attention_ex(
  *                1024 forces a number.  The query rows whose keys a boundary
  *                cuts leave unrounded results in the workspace, which a second
  *                kernel merges by log-sum-exp.  The workspace (any contents,
- *                16-byte aligned, this call's alone until it has run) holds
+ *                32-byte aligned, this call's alone until it has run) holds
  *                pgd_prefill_workspace_bytes(...) bytes; with num_ctas = 0 and
  *                a smaller one or NULL nothing is cut, with num_ctas > 1 the
  *                call returns PGD_ERR_WORKSPACE

@@ -90,11 +90,11 @@ static cudaError_t launch(const PrefillLaunch &a) {
     static const bool fits = [&] {
         cudaFuncAttributes f;
         return cudaFuncGetAttributes(&f, kernel) == cudaSuccess &&
-               f.numRegs * kPrefillThreads >= kSoftmaxRegs * 256 + kOtherRegs * 128;
+               f.numRegs * C::THREADS >= C::SOFTMAX_REGS * 256 + C::OTHER_REGS * (C::THREADS - 256);
     }();
     if (!fits) return cudaErrorLaunchOutOfResources;
     const PrefillMaps maps = {a.map_q, a.map_k, a.map_v};
-    kernel<<<a.grid, kPrefillThreads, C::SMEM, a.stream>>>(maps, a.p);
+    kernel<<<a.grid, C::THREADS, C::SMEM, a.stream>>>(maps, a.p);
     e = cudaGetLastError();
     if (e != cudaSuccess || !a.p.parts || a.grid < 2) return e;
     cudaLaunchAttribute attr[1];

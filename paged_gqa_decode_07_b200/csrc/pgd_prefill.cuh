@@ -16,17 +16,19 @@
 // A unit that a boundary cuts leaves one unrounded piece per CTA in the
 // workspace; a second kernel merges them by log-sum-exp.
 //
-// CTA = 2 softmax warpgroups + one of four single warps:
+// CTA = 2 softmax warpgroups + single warps:
 //   warps 0-3, 4-7   softmax; thread = query row (one TMEM lane)
 //   warp 8           finds the share, hands its pieces out, and loads: Q and
 //                    [128 keys x 128 dims] boxes of K and V into a ring (TMA)
-//   warp 9           issues the tcgen05.mma of S = Q K^T and O += P V
-//   warps 10, 11     keep masked keys out of V (below); for FP8 caches they
+//   warp 9           issues the tcgen05.mma of S = Q K^T and O += P V, the
+//                    query tiles in turn (a warp for each let the tiles fall
+//                    into step: both in softmax, then both at the tensor cores)
+//   the last 2 or 4  keep masked keys out of V (below); for FP8 caches they
 //                    also turn the E4M3 boxes and the query rows into f16
 // S, P and O live in tensor memory (512 columns):
-//   NQ = 2: S0 | S1 | O0 | O1, P_t in the columns of S_t.  The two tiles take
-//     turns: one's softmax runs while the other's products do, and S_t(j + 1)
-//     follows P_t(j) V(j) in issue order, so S_t ready means O_t is at rest.
+//   NQ = 2: S0 | S1 | O0 | O1, P_t in the columns of S_t.  One tile's softmax
+//     runs while the other's products do, and S_t(j + 1) follows P_t(j) V(j)
+//     in issue order, so S_t ready means O_t is at rest.
 //   NQ = 1: S0 | S1 | O (256): S(j + 1) is formed while softmax(j) runs.
 //
 // Softmax, one pass with a running reference m and sum l in fp32: the weights
@@ -56,25 +58,28 @@ namespace pgd {
 constexpr uint32_t kLine = 128 * 128;         // bytes of a line: 128 rows x 128 B
 constexpr uint32_t kBox = 2 * kLine;          // [128 keys][128 dims], 16-bit
 constexpr uint32_t kRawBox = kLine;           // [128 keys][128 dims], 8-bit
-// Of every 8 pairs of exponentials, how many are computed with FMAs.
-constexpr int kPolyOf8 = 2;
 constexpr int kRedoSlots = 8;
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;   // 8 warps and 4: 12 x 168 in all
 constexpr uint32_t kMetaBytes = 1024;
 
+// Warps 0-7 are the softmax warpgroups; an FP8 cache takes more warps to
+// convert.  Registers: 8 x 184 + 4 x 136 = 12 x 168, 8 x 152 + 8 x 104 = 16 x 128.
 template <int D, bool FP8>
 struct PrefillCfg {
+    static constexpr int THREADS = FP8 ? 512 : 384;
+    static constexpr int SOFTMAX_REGS = FP8 ? 152 : 184, OTHER_REGS = FP8 ? 104 : 136;
+    static constexpr int V_WARPS = FP8 ? 4 : 2;
+    static constexpr int V_WARP0 = THREADS / 32 - V_WARPS;
+    static_assert(SOFTMAX_REGS * 256 + OTHER_REGS * (THREADS - 256) <=
+                  65536 / THREADS / 8 * 8 * THREADS, "registers of the launch");
     static constexpr int NQ = D == 128 ? 2 : 1;
     static constexpr int LINES = D / 64;              // lines of a Q tile
     static constexpr int BOXES = D / 128;             // boxes of a K or V tile
     static constexpr uint32_t QTILE = LINES * kLine;
-    static constexpr int NS = FP8 ? 3 : 4;            // ring of 16-bit boxes
-    static constexpr int NR = FP8 ? 2 : 0;            // ring of raw E4M3 boxes
-    static constexpr uint32_t STAGE = NQ * 4 * 4096;  // outputs on their way out, 4 KB a warp
+    static constexpr int NS = FP8 ? 3 : 5;            // ring of 16-bit boxes
+    static constexpr int NR = FP8 ? 4 : 0;            // ring of raw E4M3 boxes
     static constexpr uint32_t OFF_RING = NQ * QTILE;
     static constexpr uint32_t OFF_RAW = OFF_RING + NS * kBox;
-    static constexpr uint32_t OFF_STAGE = OFF_RAW + NR * kRawBox;
-    static constexpr uint32_t OFF_META = OFF_STAGE + STAGE;
+    static constexpr uint32_t OFF_META = OFF_RAW + NR * kRawBox;
     static constexpr uint32_t SMEM = OFF_META + kMetaBytes + (FP8 ? 2048 : 0);
     static_assert(SMEM <= 232448, "more shared memory than a CTA has");
 };
@@ -83,9 +88,9 @@ struct PrefillCfg {
 // the query rows follow).
 struct PrefillMeta {
     uint64_t q_full, q_ready, q_empty, drain, pv_done;
-    uint64_t s_ready[2], p_ready[2][2], o_done[2], o_free[2];
-    uint64_t full[4], empty[4], fixed[4];
-    uint64_t raw_full[3], raw_empty[3];
+    uint64_t s_ready[2], p_ready[2][2], o_done[2];
+    uint64_t full[5], empty[5], fixed[5];
+    uint64_t raw_full[4], raw_empty[4];
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     Piece piece[kPieces];
     Share share;
@@ -97,47 +102,24 @@ struct PrefillMaps {
     CUtensorMap q, k, v;
 };
 
-// The keys that each query tile of a piece sees.
-struct TileKeys {
-    int ntok;           // query tokens of the tile
-    int p0;             // position of the first
-    int kb, ke;         // key tiles of this piece
-    int mlo, mhi;       // tiles below mlo or from mhi on are not seen whole by every row
-};
+// Whether some row of an active tile does not see all of key tile j (the
+// tiles' ranges leave no gap).
+__device__ __forceinline__ bool is_partial(const Piece &k, int j) {
+    return j < k.part_lo || j >= k.part_hi;
+}
 
+// Fill in what each query tile of a piece sees (the producer, once a piece).
 template <int NQ>
-struct UnitKeys {
-    TileKeys t[NQ];
-    int kb, ke;
-    int lo, hi;         // positions that some row sees (whole unit)
-    int all_lo, all_hi; // positions that every row sees
-    int part_lo, part_hi;
-
-    __device__ __forceinline__ bool active(int i, int j) const {
-        return j >= t[i].kb && j < t[i].ke;
-    }
-    // whether some row of query tile i does not see all of key tile j
-    __device__ __forceinline__ bool masked(int i, int j) const {
-        return j < t[i].mlo || j >= t[i].mhi;
-    }
-    // the same for the unit's active tiles (their ranges leave no gap)
-    __device__ __forceinline__ bool partial(int j) const { return j < part_lo || j >= part_hi; }
-};
-
-template <int NQ>
-__device__ __forceinline__ UnitKeys<NQ> unit_keys(const PrefillParams &p, const Piece &u, int tpq) {
-    UnitKeys<NQ> k;
-    k.kb = u.kb;
-    k.ke = u.ke;
-    k.hi = u.pos0 + u.ntok;
-    k.lo = p.window > 0 ? max(0, u.pos0 + 1 - p.window) : 0;
-    k.all_hi = u.pos0 + 1;
-    k.all_lo = p.window > 0 ? k.hi - p.window : 0;
-    k.part_lo = 0;
-    k.part_hi = 0x7fffffff;
+__device__ __forceinline__ void piece_keys(const PrefillParams &p, Piece &u, int tpq) {
+    u.hi = u.pos0 + u.ntok;
+    u.lo = p.window > 0 ? max(0, u.pos0 + 1 - p.window) : 0;
+    u.all_hi = u.pos0 + 1;
+    u.all_lo = p.window > 0 ? u.hi - p.window : 0;
+    u.part_lo = 0;
+    u.part_hi = 0x7fffffff;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-        TileKeys &t = k.t[i];
+        TileKeys &t = u.t[i];
         t.ntok = min(tpq, u.ntok - i * tpq);
         t.p0 = u.pos0 + i * tpq;
         t.kb = t.ke = t.mlo = t.mhi = 0;
@@ -147,24 +129,24 @@ __device__ __forceinline__ UnitKeys<NQ> unit_keys(const PrefillParams &p, const 
             t.ke = max(t.kb, min((hi + kKeys - 1) / kKeys, u.ke));
             t.mlo = p.window > 0 ? (max(0, hi - p.window) + kKeys - 1) / kKeys : 0;
             t.mhi = max(0, t.p0 + 1) / kKeys;
-            k.part_lo = max(k.part_lo, t.mlo);
-            k.part_hi = min(k.part_hi, t.mhi);
+            u.part_lo = max(u.part_lo, t.mlo);
+            u.part_hi = min(u.part_hi, t.mhi);
         }
     }
-    return k;
 }
 
 // ---------------------------------------------------------------- the V warps
 // Keep masked keys out of a 16-bit V box: zero the rows outside [lo, hi) of
 // the tile's keys, and tell whether one that only some query rows see, outside
-// [all_lo, all_hi), holds a non-finite value.  64 threads, 8 of them on one
-// row's 128-byte line.
+// [all_lo, all_hi), holds a non-finite value.  8 threads on one row's 128-byte
+// line.
+template <int WARPS>
 __device__ __forceinline__ bool clean_box(uint32_t box, int lo, int hi, int all_lo, int all_hi,
                                           int tid) {
     bool bad = false;
     const uint32_t at = box + (tid & 7) * 16;
     const int r0 = tid >> 3;
-    for (int r = r0; r < 128; r += 8) {
+    for (int r = r0; r < 128; r += WARPS * 4) {
         if (r >= all_lo && r < all_hi) continue;
         const uint32_t a = at + r * 128;
         if (r < lo || r >= hi) {
@@ -184,10 +166,11 @@ __device__ __forceinline__ bool clean_box(uint32_t box, int lo, int hi, int all_
 
 // A raw E4M3 box to f16 (both with the 128-byte swizzle); as clean_box for
 // rows outside [lo, hi), which become zeros without being looked at.
+template <int WARPS>
 __device__ __forceinline__ bool convert_box(uint32_t raw, uint32_t box, int lo, int hi, int tid) {
     bool bad = false;
 #pragma unroll 4
-    for (int i = tid; i < 128 * 8; i += 64) {
+    for (int i = tid; i < 128 * 8; i += 32 * WARPS) {
         const int r = i >> 3, c = i & 7, sw = r & 7;
         uint32_t x[4];
         lds128(raw + r * 128 + ((c ^ sw) << 4), x[0], x[1], x[2], x[3]);
@@ -258,35 +241,13 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     return r;
 }
 
-// 2^x of a pair (x <= 9, or NaN, whose result is any number: the row's sum is
-// NaN already).  x = n + f with n the nearest integer, read off the low bits
-// of x + 1.5 * 2^23; 2^f on [-1/2, 1/2] by the polynomial of degree 5 with
-// constant term 1 and the least largest relative error (fitted by linear
-// programming; 2^-22.5 with its fp32 roundings), n added to the exponent.  At
-// the clamp, x = -127, f is 0 and the sum of the bits is 0 exactly: what a
-// mask set to -infinity weighs nothing.
-__device__ __forceinline__ float2 exp2_poly2(float2 x) {
-    const float2 magic = make_float2(12582912.f, 12582912.f), back = make_float2(-12582912.f, -12582912.f);
-    x.x = fmaxf(x.x, -127.f);
-    x.y = fmaxf(x.y, -127.f);
-    const float2 n = add2(x, magic);
-    const float2 f = fma2(add2(n, back), make_float2(-1.f, -1.f), x);
-    float2 q = make_float2(0.001326472731307149f, 0.001326472731307149f);
-    q = fma2(q, f, make_float2(0.009671512991189957f, 0.009671512991189957f));
-    q = fma2(q, f, make_float2(0.05550733581185341f, 0.05550733581185341f));
-    q = fma2(q, f, make_float2(0.24022242426872253f, 0.24022242426872253f));
-    q = fma2(q, f, make_float2(0.6931470036506653f, 0.6931470036506653f));
-    q = fma2(q, f, make_float2(1.f, 1.f));
-    return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(n.x) << 23)),
-                       __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(n.y) << 23)));
-}
-
 // ---------------------------------------------------------------- the kernel
 // A warp's wait for a phase, all lanes or none: false when `limit_ns` ran out
-// (the timeout flag is raised).  One short loop: the kernel's loops run from
-// the small instruction caches, and there are many waits.
+// (the timeout flag is raised).  A phase that is over costs 50 cycles; every
+// branch or 64-bit compare before the test showed (180 with four of them).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                           uint32_t *flags) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
     const uint32_t nap = limit_ns < 20000 ? static_cast<uint32_t>(limit_ns) : 20000u;
     uint64_t t0 = 0;
     while (!__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, nap))) {
@@ -301,7 +262,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
 }
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kPrefillThreads, 1)
+__global__ void __launch_bounds__((PrefillCfg<D, FP8>::THREADS), 1)
 prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) {
     using C = PrefillCfg<D, FP8>;
     constexpr int NQ = C::NQ;
@@ -319,7 +280,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
 
     if (threadIdx.x == 0) {
         mbar_init(bar(meta.q_full), 1);
-        mbar_init(bar(meta.q_ready), 2);
+        mbar_init(bar(meta.q_ready), C::V_WARPS);
         mbar_init(bar(meta.q_empty), 1);
         mbar_init(bar(meta.drain), 1);
         mbar_init(bar(meta.pv_done), 1);
@@ -328,22 +289,21 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             mbar_init(bar(meta.p_ready[i][0]), 4);
             mbar_init(bar(meta.p_ready[i][1]), 4);
             mbar_init(bar(meta.o_done[i]), 1);
-            mbar_init(bar(meta.o_free[i]), 4);
+        }
+        for (int i = 0; i < 5; ++i) {
+            // 16-bit ring: filled by TMA and read by the MMA and the V warps,
+            // or (FP8) filled by the V warps and read by the MMA
+            mbar_init(bar(meta.full[i]), FP8 ? C::V_WARPS : 1);
+            mbar_init(bar(meta.empty[i]), FP8 ? 1 : 1 + C::V_WARPS);
+            mbar_init(bar(meta.fixed[i]), C::V_WARPS);
         }
         for (int i = 0; i < 4; ++i) {
-            // 16-bit ring: filled by TMA and read by the MMA and the V warps,
-            // or (FP8) filled by the two V warps and read by the MMA
-            mbar_init(bar(meta.full[i]), FP8 ? 2 : 1);
-            mbar_init(bar(meta.empty[i]), FP8 ? 1 : 3);
-            mbar_init(bar(meta.fixed[i]), 2);
-        }
-        for (int i = 0; i < 3; ++i) {
             mbar_init(bar(meta.raw_full[i]), 1);
-            mbar_init(bar(meta.raw_empty[i]), 2);
+            mbar_init(bar(meta.raw_empty[i]), C::V_WARPS);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(bar(meta.piece_full[i]), 1);
-            mbar_init(bar(meta.piece_empty[i]), 3 + 4 * NQ);   // MMA, V and softmax warps
+            mbar_init(bar(meta.piece_empty[i]), 1 + 4 * NQ + C::V_WARPS);   // MMA, softmax, V warps
         }
         for (int i = 0; i < kRedoSlots; ++i) meta.redo[i] = 0;
         fence_mbar_init();
@@ -352,7 +312,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         tma_prefetch_desc(&maps.v);
     }
     if (warp == 9) tmem_alloc(smem_u32(&meta.tmem), 512);
-    find_share<NQ>(p, meta.share);               // meets at __syncthreads
+    find_share<NQ, C::THREADS>(p, meta.share);               // meets at __syncthreads
     tcgen05_fence_before();
     __syncthreads();
     tcgen05_fence_after();
@@ -360,7 +320,6 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
     constexpr uint32_t kOCol = 256;              // O_t at kOCol + t * 128
     const int tpq = 128 / p.group;
     const uint64_t limit = p.wait_ns;
-    Piece u;
     int piece = 0;
 
     const auto wait = [&](uint64_t &b, uint32_t parity) {
@@ -368,17 +327,17 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
     };
     // the next piece handed out by the producer; false at the end
     const auto next_piece = [&]() {
-        const int s = piece % kPieces;
-        if (!wait(meta.piece_full[s], (piece / kPieces) & 1)) return false;
-        ++piece;
-        u = meta.piece[s];
+        return wait(meta.piece_full[piece % kPieces], (piece / kPieces) & 1) &&
+               meta.piece[piece % kPieces].ntok > 0;
+    };
+    const auto piece_read = [&]() {
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(meta.piece_empty[s]));
-        return u.ntok > 0;
+        if (lane == 0) mbar_arrive(bar(meta.piece_empty[piece % kPieces]));
+        ++piece;
     };
 
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == 8) {
         // ================================================== producer
         constexpr int N = FP8 ? C::NR : C::NS;
@@ -392,8 +351,10 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         bool ok = true;
         PieceWalk<NQ> walk(p, meta.share);
         while (ok) {
+            Piece u;
             const bool more = walk.next(u);
-            if (!more) u.ntok = 0;
+            if (more) piece_keys<NQ>(p, u, tpq);
+            else u.ntok = 0;
             if (!(ok = wait(meta.piece_empty[piece % kPieces], ((piece / kPieces) & 1) ^ 1))) break;
             if (lane == 0) {
                 meta.piece[piece % kPieces] = u;
@@ -401,14 +362,13 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             }
             ++piece;
             if (!more) break;
-            const UnitKeys<NQ> k = unit_keys<NQ>(p, u, tpq);
-            if (k.kb >= k.ke) continue;
+            if (u.kb >= u.ke) continue;
             const int32_t *table = p.block_table + static_cast<int64_t>(u.seq) * p.max_blocks_per_seq;
             // block ids of key tile j: lane b % nblk holds block b's (or -1)
             const auto ids = [&](int j) {
-                if (!paged || j >= k.ke) return -1;
+                if (!paged || j >= u.ke) return -1;
                 const int key = j * kKeys + (lane % nblk) * bs;
-                if (key + bs <= k.lo || key >= k.hi) return -1;
+                if (key + bs <= u.lo || key >= u.hi) return -1;
                 int id = __ldg(table + key / bs);
                 if (id < 0 || id >= p.num_blocks) {
                     raise_flag(p.flags, kFlagBlockId);
@@ -445,13 +405,13 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                 __syncwarp();
                 return true;
             };
-            int id = ids(k.kb), id_next = ids(k.kb + 1);
+            int id = ids(u.kb), id_next = ids(u.kb + 1);
             if (!(ok = wait(meta.q_empty, (units & 1) ^ 1))) break;
             ++units;
             if (lane == 0) {
                 const uint32_t b = bar(meta.q_full);
                 int tiles = 0;
-                for (int i = 0; i < NQ; ++i) tiles += k.t[i].ntok > 0;
+                for (int i = 0; i < NQ; ++i) tiles += u.t[i].ntok > 0;
                 mbar_arrive_expect_tx(b, tiles * C::LINES * tpq * p.group * 128);
                 for (int i = 0; i < tiles; ++i)
                     for (int l = 0; l < C::LINES; ++l)
@@ -460,17 +420,17 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             }
             __syncwarp();
             if (NQ == 2) {
-                for (int j = k.kb; ok && j < k.ke; ++j) {
+                for (int j = u.kb; ok && j < u.ke; ++j) {
                     const int id2 = ids(j + 2);
                     ok = load(&maps.k, j, 0, id) && load(&maps.v, j, 0, id);
                     id = id_next;
                     id_next = id2;
                 }
             } else {
-                for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.k, k.kb, b, id);
-                for (int j = k.kb; ok && j < k.ke; ++j) {
+                for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.k, u.kb, b, id);
+                for (int j = u.kb; ok && j < u.ke; ++j) {
                     const int id2 = ids(j + 2);
-                    if (j + 1 < k.ke)
+                    if (j + 1 < u.ke)
                         for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.k, j + 1, b, id_next);
                     for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.v, j, b, id);
                     id = id_next;
@@ -492,45 +452,45 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         const uint32_t leader = elect_one();
         int units = 0, steps = 0, slot = 0;
         uint32_t phase = 0, fixed_phase = 0;
-        uint32_t counts = 0;        // parities of the tiles' P (bits 0, 8) and O (bits 4, 12)
+        uint32_t p_count = 0;                        // parities, bit t of tile t
         bool ok = true;
         // S columns <- Q tile i . K box in slot s, elements 128 * half ...
         const auto qk = [&](uint32_t d, int i, int s, int half) {
-            const uint32_t a = smem + i * C::QTILE + half * kBox, b = ring + s * kBox;
+            const uint64_t a = smem_desc(smem + i * C::QTILE + half * kBox, 16);
+            const uint64_t b = smem_desc(ring + s * kBox, 16);
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t off = (kk >> 2) * kLine + (kk & 3) * 32;
-                mma_ss(leader, tmem + d, smem_desc(a + off, 16, 1024),
-                       smem_desc(b + off, 16, 1024), kIdS, half > 0 || kk > 0);
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t off = ((kk >> 2) * kLine + (kk & 3) * 32) >> 4;
+                    mma_ss(tmem + d, a + off, b + off, kIdS, kk > 0 || half > 0);
+                }
             }
         };
         // O columns (+)= P (in S columns c) . V box in slot s, one half of the keys
         const auto pv = [&](uint32_t d, uint32_t c, int s, int half, bool acc) {
-            const uint32_t b = ring + s * kBox;
+            const uint64_t b = smem_desc(ring + s * kBox + half * 8192, kLine);
+            const uint32_t a = tmem + c + half * 32;
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_ts(leader, tmem + d, tmem + c + (4 * half + kk) * 8,
-                       smem_desc(b + (4 * half + kk) * 2048, kLine, 1024), kIdO,
-                       acc || half > 0 || kk > 0);
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ts(tmem + d, a + kk * 8, b + kk * (2048 >> 4), kIdO, kk > 0 || acc);
+            }
         };
         // the ring's next box; its slot is returned, -1 after a timeout
         const auto next_box = [&](bool fix) {
             const int s = slot;
-            bool got;
-            if (fix && !FP8) {
-                got = wait(meta.fixed[s], (fixed_phase >> s) & 1);
-                fixed_phase ^= 1u << s;
-            } else {
-                got = wait(meta.full[s], phase);
-            }
+            const bool fixed = fix && !FP8;
+            const uint32_t parity = fixed ? (fixed_phase >> s) & 1 : phase;
+            if (fixed) fixed_phase ^= 1u << s;
             if (++slot == C::NS) {
                 slot = 0;
                 phase ^= 1;
             }
-            return got ? s : -1;
+            return wait(fixed ? meta.fixed[s] : meta.full[s], parity) ? s : -1;
         };
         while (ok && next_piece()) {
-            const UnitKeys<NQ> k = unit_keys<NQ>(p, u, tpq);
+            const Piece k = meta.piece[piece % kPieces];
+            piece_read();
             if (k.kb >= k.ke) continue;
             if (!(ok = wait(FP8 ? meta.q_ready : meta.q_full, units & 1))) break;
             ++units;
@@ -538,55 +498,87 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                 int sk = next_box(false);
                 ok = sk >= 0;
                 if (!ok) break;
-                tcgen05_fence_after();
-#pragma unroll
+                const int kb0 = k.t[0].kb, ke0 = k.t[0].ke;
+                const int kb1 = k.t[NQ - 1].kb, ke1 = k.t[NQ - 1].ke;
+#pragma unroll 1
                 for (int i = 0; i < NQ; ++i)
-                    if (k.active(i, k.kb)) {
+                    if (i ? kb1 == k.kb && kb1 < ke1 : kb0 == k.kb && kb0 < ke0) {
                         qk(i * 128, i, sk, 0);
-                        mma_commit(leader, bar(meta.s_ready[i]));
+                        if (leader) mma_commit(bar(meta.s_ready[i]));
                     }
-                mma_commit(leader, bar(meta.empty[sk]));
-                if (k.kb + 1 == k.ke) mma_commit(leader, bar(meta.q_empty));
-                for (int j = k.kb; j < k.ke; ++j) {
+                if (leader) mma_commit(bar(meta.empty[sk]));
+                if (leader && k.kb + 1 == k.ke) mma_commit(bar(meta.q_empty));
+                // steps in which both tiles finish one key tile and start the
+                // next, and nothing else happens, run without conditions
+                const int steady_lo = max(max(kb0, kb1) + 1, k.part_lo);
+                const int steady_hi = min(min(ke0, ke1), k.part_hi) - 2;
+                for (int j = k.kb; ok && j < k.ke; ++j) {
+                    if (j >= steady_lo && j < steady_hi) {
+                        const int sv = slot, sn = slot + 1 == C::NS ? 0 : slot + 1;
+                        const uint32_t next_phase = phase ^ (slot + 1 == C::NS);
+                        ok = false;
+                        if (!wait(meta.full[sv], phase)) break;
+                        if (!wait(meta.p_ready[0][0], p_count & 1)) break;
+                        tcgen05_fence_after();
+                        pv(kOCol, 0, sv, 0, true);
+                        if (!wait(meta.p_ready[0][1], p_count & 1)) break;
+                        tcgen05_fence_after();
+                        pv(kOCol, 0, sv, 1, true);
+                        if (!wait(meta.full[sn], next_phase)) break;
+                        qk(0, 0, sn, 0);
+                        if (leader) mma_commit(bar(meta.s_ready[0]));
+                        if (!wait(meta.p_ready[1][0], p_count >> 1)) break;
+                        tcgen05_fence_after();
+                        pv(kOCol + 128, 128, sv, 0, true);
+                        if (!wait(meta.p_ready[1][1], p_count >> 1)) break;
+                        tcgen05_fence_after();
+                        pv(kOCol + 128, 128, sv, 1, true);
+                        if (leader) mma_commit(bar(meta.empty[sv]));
+                        qk(128, 1, sn, 0);
+                        if (leader) {
+                            mma_commit(bar(meta.s_ready[1]));
+                            mma_commit(bar(meta.empty[sn]));
+                        }
+                        p_count ^= 3;
+                        slot = sn + 1 == C::NS ? 0 : sn + 1;
+                        phase = next_phase ^ (sn + 1 == C::NS);
+                        ok = true;
+                        continue;
+                    }
                     const bool more = j + 1 < k.ke;
-                    const int sv = next_box(k.partial(j));
+                    const int sv = next_box(is_partial(k, j));
                     ok = sv >= 0;
-                    if (ok && more) {
-                        sk = next_box(false);
-                        ok = sk >= 0;
-                    }
                     if (!ok) break;
 #pragma unroll 1
                     for (int i = 0; i < NQ; ++i) {
-                        const int kb = i ? k.t[NQ - 1].kb : k.t[0].kb;
-                        const int ke = i ? k.t[NQ - 1].ke : k.t[0].ke;
+                        const int kb = i ? kb1 : kb0, ke = i ? ke1 : ke0;
                         if (j >= kb && j < ke) {
-                            const uint32_t n = counts >> (8 * i);      // S tiles so far, O tiles so far
-                            if (j == kb) ok = wait(meta.o_free[i], ((n >> 4) & 1) ^ 1);
 #pragma unroll 1
                             for (int h = 0; h < 2; ++h) {
-                                ok = ok && wait(meta.p_ready[i][h], n & 1);
+                                ok = wait(meta.p_ready[i][h], (p_count >> i) & 1);
                                 if (!ok) break;
                                 tcgen05_fence_after();
-                                pv(kOCol + i * 128, i * 128, sv, h, j > kb);
+                                pv(kOCol + i * 128, i * 128, sv, h, h > 0 || j > kb);
                             }
                             if (!ok) break;
-                            counts ^= 1u << (8 * i);
-                            if (j + 1 == ke) {
-                                mma_commit(leader, bar(meta.o_done[i]));
-                                counts ^= 16u << (8 * i);
-                            }
+                            p_count ^= 1u << i;
+                            if (j + 1 == ke && leader) mma_commit(bar(meta.o_done[i]));
                         }
-                        if (i == NQ - 1) mma_commit(leader, bar(meta.empty[sv]));
+                        if (i == NQ - 1 && leader) mma_commit(bar(meta.empty[sv]));
+                        if (i == 0 && more) {
+                            sk = next_box(false);
+                            ok = sk >= 0;
+                            if (!ok) break;
+                        }
                         if (j + 1 >= kb && j + 1 < ke) {
                             qk(i * 128, i, sk, 0);
-                            mma_commit(leader, bar(meta.s_ready[i]));
+                            if (leader) mma_commit(bar(meta.s_ready[i]));
                         }
                     }
                     if (!ok) break;
-                    if (more) {
-                        mma_commit(leader, bar(meta.empty[sk]));
-                        if (j + 2 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                    if (leader && more) {
+                        mma_commit(bar(meta.empty[sk]));
+                        if (j + 2 == k.ke) mma_commit(bar(meta.q_empty));
                     }
                 }
             } else {
@@ -594,24 +586,24 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                     for (int b = 0; b < C::BOXES; ++b) {
                         const int s = next_box(false);
                         if (s < 0) return false;
-                        tcgen05_fence_after();
                         qk((step & 1) * 128, 0, s, b);
-                        mma_commit(leader, bar(meta.empty[s]));
+                        if (leader) {
+                            mma_commit(bar(meta.empty[s]));
+                            if (b == C::BOXES - 1) mma_commit(bar(meta.s_ready[step & 1]));
+                        }
                     }
-                    mma_commit(leader, bar(meta.s_ready[step & 1]));
                     return true;
                 };
                 ok = qk_tile(steps);
-                if (ok && k.kb + 1 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                if (ok && k.kb + 1 == k.ke && leader) mma_commit(bar(meta.q_empty));
                 for (int j = k.kb; ok && j < k.ke; ++j, ++steps) {
                     if (j + 1 < k.ke) {
                         if (!(ok = qk_tile(steps + 1))) break;
-                        if (j + 2 == k.ke) mma_commit(leader, bar(meta.q_empty));
+                        if (j + 2 == k.ke && leader) mma_commit(bar(meta.q_empty));
                     }
-                    if (j == k.kb) ok = wait(meta.o_free[0], ((counts >> 4) & 1) ^ 1);
 #pragma unroll 1
                     for (int b = 0; b < C::BOXES; ++b) {
-                        const int s = next_box(k.partial(j));
+                        const int s = next_box(is_partial(k, j));
                         ok = ok && s >= 0;
 #pragma unroll 1
                         for (int h = 0; h < 2; ++h) {
@@ -619,34 +611,34 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                                 ok = ok && wait(meta.p_ready[steps & 1][h], (steps >> 1) & 1);
                             if (!ok) break;
                             tcgen05_fence_after();
-                            pv(kOCol + b * 128, (steps & 1) * 128, s, h, j > k.kb);
+                            pv(kOCol + b * 128, (steps & 1) * 128, s, h, h > 0 || j > k.kb);
                         }
                         if (!ok) break;
-                        mma_commit(leader, bar(meta.empty[s]));
+                        if (leader) mma_commit(bar(meta.empty[s]));
                     }
                     if (!ok) break;
-                    mma_commit(leader, bar(meta.pv_done));
-                    if (j + 1 == k.ke) mma_commit(leader, bar(meta.o_done[0]));
+                    if (leader) mma_commit(bar(meta.pv_done));
+                    if (j + 1 == k.ke && leader) mma_commit(bar(meta.o_done[0]));
                 }
-                counts ^= 16;
             }
         }
         // the tensor cores must be done with shared and tensor memory
-        mma_commit(leader, bar(meta.drain));
+        if (leader) mma_commit(bar(meta.drain));
         if (!mbar_wait_bounded(bar(meta.drain), 0, kDrainWaitNs)) raise_flag(p.flags, kFlagTimeout);
         __syncwarp();
-    } else if (warp >= 10) {
+    } else if (warp >= C::V_WARP0) {
         // ================================================== V warps
-        const int tid = threadIdx.x - 320;
+        const int tid = threadIdx.x - C::V_WARP0 * 32;
         int box = 0, units = 0;
         bool ok = true;
         while (ok && next_piece()) {
-            const UnitKeys<NQ> k = unit_keys<NQ>(p, u, tpq);
+            const Piece k = meta.piece[piece % kPieces];
+            piece_read();
             if (k.kb >= k.ke) continue;
             if (FP8) {
                 if (!(ok = wait(meta.q_full, units & 1))) break;
-                for (int r = tid; r < NQ * 128; r += 64) {
-                    if (k.t[(r >> 7) % NQ].ntok > 0)
+                for (int r = tid; r < NQ * 128; r += 32 * C::V_WARPS) {
+                    if (r < 128 || k.t[NQ - 1].ntok > 0)
                         row_mult[(units & 1) * 256 + r] =
                             convert_q_row(smem + (r >> 7) * C::QTILE, r & 127);
                 }
@@ -658,7 +650,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             // one box: j its key tile, v whether it is of V
             const auto take = [&](int j, bool v) {
                 const int s = box % C::NS;
-                const bool part = v && k.partial(j);
+                const bool part = v && is_partial(k, j);
                 const int j0 = j * kKeys;
                 const int lo = part ? k.lo - j0 : 0, hi = part ? k.hi - j0 : kKeys;
                 bool bad = false;
@@ -666,7 +658,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                     const int r = box % (FP8 ? C::NR : 1);
                     if (!wait(meta.raw_full[r], (box / (FP8 ? C::NR : 1)) & 1)) return false;
                     if (!wait(meta.empty[s], ((box / C::NS) & 1) ^ 1)) return false;
-                    bad = convert_box(raw_ring + r * kRawBox, ring + s * kBox, lo, hi, tid);
+                    bad = convert_box<C::V_WARPS>(raw_ring + r * kRawBox, ring + s * kBox, lo, hi, tid);
                     fence_proxy_async();
                     if (part && bad) meta.redo[units % kRedoSlots] = units;
                     __syncwarp();
@@ -677,7 +669,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                 } else {
                     if (!wait(meta.full[s], (box / C::NS) & 1)) return false;
                     if (part) {
-                        bad = clean_box(ring + s * kBox, lo, hi, k.all_lo - j0, k.all_hi - j0, tid);
+                        bad = clean_box<C::V_WARPS>(ring + s * kBox, lo, hi, k.all_lo - j0, k.all_hi - j0, tid);
                         fence_proxy_async();
                         if (bad) meta.redo[units % kRedoSlots] = units;
                         __syncwarp();
@@ -702,7 +694,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         }
     }
     } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX_REGS));
     if (NQ == 2 || warp < 4) {
         // ================================================== softmax
         const int t = NQ == 2 ? warp >> 2 : 0;
@@ -713,10 +705,11 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         constexpr float kLog2e = 1.4426950408889634f;
         int units = 0, steps = 0, done = 0;
         bool ok = true;
-        while (ok && next_piece()) {
-            const UnitKeys<NQ> k = unit_keys<NQ>(p, u, tpq);
-            if (k.kb < k.ke) ++units;
-            const TileKeys &tk = k.t[t];
+        // the piece stays in shared memory until its output is out
+        for (; ok && next_piece(); piece_read()) {
+            const Piece &u = meta.piece[piece % kPieces];
+            const TileKeys tk = u.t[t];
+            if (u.kb < u.ke) ++units;
             if (tk.ntok <= 0) continue;
             const bool valid = tok < tk.ntok;
             const int hi = tk.p0 + tok + 1;
@@ -738,7 +731,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                         // and masked scores (-inf) must still vanish
                         if (mult == 0.f) mult = 0x1p-126f;
                     }
-                    const bool masked = k.masked(t, j);
+                    const bool masked = j < tk.mlo || j >= tk.mhi;
                     if (__any_sync(0xffffffffu, masked || mult < 0.f)) {
                         // scores are changed where they lie: hidden ones to
                         // -inf, and all of them negated for a negative scale;
@@ -761,22 +754,23 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                         }
                         tmem_wait_st();
                     }
-                    float mx = -INFINITY;
-                    {
-                        float s[128];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld32(scol + c * 32, s + c * 32);
+                    // row maximum
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int c0 = 0; c0 < 128; c0 += 64) {
+                        float s[64];
+                        tmem_ld32(scol + c0, s);
+                        tmem_ld32(scol + c0 + 32, s + 32);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 128; ++c) asm volatile("" : "+f"(s[c]));
-                        float m4[4] = {mx, mx, mx, mx};
+                        for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(s[c]));
 #pragma unroll
-                        for (int c = 0; c < 128; c += 8)
+                        for (int c = 0; c < 64; c += 8)
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 m4[i] = max3_nan(m4[i], s[c + i], s[c + 4 + i]);
-                        mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
                     }
+                    const float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
                     const float am = fabsf(mult);
                     const float top = valid ? mx * am : -INFINITY;
                     // also for NaN, which poisons the row's sum, and +inf
@@ -809,33 +803,35 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                     }
                     const float mu = m == -INFINITY ? 0.f : -m;
                     const float2 k2 = make_float2(am, am), m2 = make_float2(mu, mu);
+                    // The scores are read a second time, in a short loop: all
+                    // warps of an SM run from one instruction cache, and with
+                    // the scores held in registers and the step unrolled it
+                    // took 3% longer; with every fourth pair of exponentials
+                    // as a polynomial on the FMA pipes 7% longer.
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float s[32];
-                        uint32_t w[16];
-                        tmem_ld32(scol + c * 32, s);
-                        tmem_wait_ld();
+                    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(s[i]));
+                        for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                            float s[32];
+                            uint32_t w[16];
+                            tmem_ld32(scol + c * 32, s);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float2 x = fma2(make_float2(s[i], s[i + 1]), k2, m2);
-                            if ((i / 2) % 8 >= 8 - kPolyOf8) {
-                                x = exp2_poly2(x);
-                            } else {
+                            for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(s[i]));
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                float2 x = fma2(make_float2(s[i], s[i + 1]), k2, m2);
                                 x.x = ex2(x.x);
                                 x.y = ex2(x.y);
+                                l2 = add2(l2, x);
+                                w[i / 2] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
                             }
-                            l2 = add2(l2, x);
-                            w[i / 2] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
+                            tmem_st16(scol + c * 16, w);
                         }
-                        tmem_st16(scol + c * 16, w);
-                        if (c & 1) {
-                            tmem_wait_st();
-                            tcgen05_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(bar(meta.p_ready[sb][c >> 1]));
-                        }
+                        tmem_wait_st();
+                        tcgen05_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(meta.p_ready[sb][h]));
                     }
                 }
                 if (!ok) break;
@@ -848,7 +844,6 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             }
             const float vs = FP8 ? __ldg(p.v_scale + u.h) : 1.f;
             if (redo) {
-                if (lane == 0) mbar_arrive(bar(meta.o_free[t]));
                 KvRows kv;
                 kv.flags = p.flags;
                 kv.head = u.h; kv.hkv = p.num_kv_heads; kv.bs = p.block_size;
@@ -894,29 +889,11 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             const bool dead = l == 0.f;
             const float inv = dead ? 0.f : vs / l;
             const float lse = dead ? -INFINITY : m * 0.6931471805599453f + logf(l);
-            // Rows leave through shared memory, 128 bytes of the warp's 32 rows
-            // at a time, so that eight lanes write one row's 128 bytes (a row
-            // per lane took 32 times the store passes).
+            // A thread writes its row, 32 bytes (a sector) at a time.
             const bool part = u.slot >= 0;
-            const int64_t row0 = part ? (static_cast<int64_t>(u.slot) * NQ + t) * 128
-                                      : static_cast<int64_t>(u.row0 + t * tpq) * p.num_q_heads + u.h * g;
-            const int rel = !valid ? -1 : part ? r : tok * p.num_q_heads + hd;
-            const uint32_t stage = smem + C::OFF_STAGE + (t * 4 + (warp & 3)) * 4096;
-            const auto put = [&](int ch, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-                sts128(stage + lane * 128 + ((ch ^ (lane & 7)) << 4), x, y, z, w);
-            };
-            const auto flush = [&](uint8_t *base, int64_t row_bytes) {
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int rr = i * 4 + (lane >> 3), ch = lane & 7;
-                    const int to = __shfl_sync(0xffffffffu, rel, rr);
-                    uint4 x;
-                    lds128(stage + rr * 128 + ((ch ^ (rr & 7)) << 4), x.x, x.y, x.z, x.w);
-                    if (to >= 0) *reinterpret_cast<uint4 *>(base + to * row_bytes + ch * 16) = x;
-                }
-                __syncwarp();
-            };
+            const int64_t orow = part ? (static_cast<int64_t>(u.slot) * NQ + t) * 128 + r
+                                      : static_cast<int64_t>(u.row0 + t * tpq + tok) * p.num_q_heads +
+                                            u.h * g + hd;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -928,30 +905,32 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                 for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(o[i]));
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = dead ? 0.f : o[i] * inv;
+                if (!valid) continue;
                 if (part) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        put(i, __float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
-                            __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
-                    flush(reinterpret_cast<uint8_t *>(p.o_part + row0 * D + c), D * 4);
+                    for (int i = 0; i < 32; i += 8)
+                        store32(p.o_part + orow * D + c + i, o + i);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        put((c & 32) / 8 + i, pack_bf16x2(o[8 * i], o[8 * i + 1]),
-                            pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
-                            pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
-                            pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-                    if (c & 32) flush(reinterpret_cast<uint8_t *>(p.out + row0 * D + c - 32), D * 2);
+                    for (int i = 0; i < 32; i += 16) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(o[i + 2 * k], o[i + 2 * k + 1]);
+                        uint16_t *dst = p.out + orow * D + c + i;
+                        if (p.out32) {
+                            store32(dst, w);
+                        } else {
+                            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
+                    }
                 }
             }
-            if (any) {
-                tcgen05_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(meta.o_free[t]));
-            }
+            // the next piece's first P, by the same warps, tells that O was read
+            tcgen05_fence_before();
             if (valid) {
-                if (part) p.lse_part[row0 + r] = lse;
-                else if (p.lse_out) p.lse_out[row0 + rel] = lse;
+                if (part) p.lse_part[orow] = lse;
+                else if (p.lse_out) p.lse_out[orow] = lse;
             }
         }
     }

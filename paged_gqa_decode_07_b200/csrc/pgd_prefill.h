@@ -33,7 +33,7 @@ struct PrefillParams {
     int32_t num_seqs, num_tokens;
     int32_t num_q_heads, num_kv_heads, group, head_dim;
     int32_t max_blocks_per_seq, block_size, num_blocks;
-    int32_t window, fp8;
+    int32_t window, fp8, out32;   // out32: out starts on 32 bytes
     float scale;
 };
 

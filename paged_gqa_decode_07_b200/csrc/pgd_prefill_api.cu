@@ -40,7 +40,7 @@ pgd_status check_common(int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
     if (num_q_heads / num_kv_heads > 16) return PGD_ERR_UNSUPPORTED;
     if (head_dim != 128 && head_dim != 256) return PGD_ERR_UNSUPPORTED;
     if (!workspace && workspace_bytes) return PGD_ERR_INVALID_ARG;
-    if (workspace && !aligned(workspace, 16)) return PGD_ERR_INVALID_ARG;
+    if (workspace && !aligned(workspace, 32)) return PGD_ERR_INVALID_ARG;
     *empty = num_seqs == 0 || num_tokens == 0;
     return PGD_OK;
 }
@@ -82,6 +82,7 @@ pgd_status run(PrefillLaunch &a, int64_t max_keys, int32_t num_ctas, void *works
         plan.cut = false;
     }
     a.grid = plan.grid;
+    p.out32 = aligned(p.out, 32);
     if (plan.cut) {
         uint8_t *w = static_cast<uint8_t *>(workspace);
         p.parts = reinterpret_cast<PartRecord *>(w);

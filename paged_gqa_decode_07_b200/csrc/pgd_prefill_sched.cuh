@@ -20,15 +20,27 @@
 
 namespace pgd {
 
-constexpr int kPrefillThreads = 384;
+constexpr int kMaxThreads = 512;
 constexpr int kKeys = 128;           // keys per tile
-constexpr int kUnitKeys = 128;       // a unit's fixed cost, in keys
+constexpr int kUnitKeys = 384;       // a unit's fixed cost, in keys
 constexpr int kPieces = 4;           // pieces handed out ahead
+
+// The keys that one query tile of a piece sees.
+struct TileKeys {
+    int ntok;           // query tokens of the tile
+    int p0;             // position of the first
+    int kb, ke;         // key tiles of this piece
+    int mlo, mhi;       // tiles below mlo or from mhi on are not seen whole by every row
+};
 
 // One CTA's part of a unit: key tiles [kb, ke) of its query tiles.
 struct Piece {
     int seq, h, row0, ntok, pos0, kv0, kb, ke;
     int slot;                        // workspace slot, -1: the whole unit
+    int lo, hi;                      // positions that some row sees (whole unit)
+    int all_lo, all_hi;              // positions that every row sees
+    int part_lo, part_hi;            // as mlo, mhi, of the tiles together
+    TileKeys t[2];
 };
 
 // Where a CTA's share starts, and how long it is.
@@ -36,7 +48,7 @@ struct Share {
     long long at, len;               // offset into the sequence's units, length
     long long seq_start;             // axis position of the sequence
     int seq;
-    long long warp_sum[kPrefillThreads / 32];
+    long long warp_sum[kMaxThreads / 32];
 };
 
 // One sequence, its query rows and its keys (zero rows: nothing to do).
@@ -94,7 +106,7 @@ __device__ __forceinline__ int tokens_per_unit(const PrefillParams &p) {
 }
 
 // The CTA's share (all threads; the caller synchronises before reading it).
-template <int NQ>
+template <int NQ, int THREADS>
 __device__ void find_share(const PrefillParams &p, Share &share) {
     const int tpu = tokens_per_unit<NQ>(p);
     const int tid = threadIdx.x, lane = tid & 31;
@@ -117,7 +129,7 @@ __device__ void find_share(const PrefillParams &p, Share &share) {
         long long before = 0;
         total = 0;
 #pragma unroll
-        for (int w = 0; w < kPrefillThreads / 32; ++w) {
+        for (int w = 0; w < THREADS / 32; ++w) {
             const long long y = share.warp_sum[w];
             if (w < (tid >> 5)) before += y;
             total += y;
@@ -128,7 +140,7 @@ __device__ void find_share(const PrefillParams &p, Share &share) {
     long long mine = len_of(tid, report), sum, total;
     long long incl = scan(mine, sum);
     total = sum;
-    for (int s0 = kPrefillThreads; s0 < p.num_seqs; s0 += kPrefillThreads) {
+    for (int s0 = THREADS; s0 < p.num_seqs; s0 += THREADS) {
         scan(len_of(s0 + tid, report), sum);
         total += sum;
     }
@@ -143,11 +155,11 @@ __device__ void find_share(const PrefillParams &p, Share &share) {
     const long long q = total / n, rest = total - q * n;   // total * n may pass 64 bits
     const long long x0 = q * c + rest * c / n, x1 = q * (c + 1) + rest * (c + 1) / n;
     long long base = 0;
-    for (int s0 = 0; s0 < p.num_seqs; s0 += kPrefillThreads) {
+    for (int s0 = 0; s0 < p.num_seqs; s0 += THREADS) {
         if (s0 > 0) {
             mine = len_of(s0 + tid, false);
             incl = scan(mine, sum);
-        } else if (p.num_seqs > kPrefillThreads) {
+        } else if (p.num_seqs > THREADS) {
             scan(mine, sum);
         }
         const long long a = base + incl - mine;
