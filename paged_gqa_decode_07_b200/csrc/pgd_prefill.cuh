@@ -322,6 +322,8 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
     const uint64_t limit = p.wait_ns;
     int piece = 0;
 
+    // the merge may be placed on SMs that this grid leaves; it waits for the end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const auto wait = [&](uint64_t &b, uint32_t parity) {
         return warp_wait(smem_u32(&b), parity, limit, p.flags);
     };

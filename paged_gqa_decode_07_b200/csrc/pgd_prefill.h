@@ -8,6 +8,9 @@
 
 namespace pgd {
 
+// Shares of the work that a call may ask for.
+constexpr int kMaxPrefillCtas = 1024;
+
 // What the merge of cut units needs to know of each CTA's start.
 struct alignas(16) PartRecord {
     long long unit;               // axis position of the unit it starts in
@@ -53,7 +56,7 @@ inline size_t prefill_workspace(int grid, int head_dim) {
 struct PrefillLaunch {
     PrefillParams p;
     CUtensorMap map_q, map_k, map_v;
-    int grid;
+    int grid, sms;
     cudaStream_t stream;
 };
 

@@ -14,9 +14,6 @@ using namespace pgd;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Shares of the work that a call may ask for.
-constexpr int32_t kMaxCtas = 1024;
-
 bool supported_block(int bs) { return bs == 16 || bs == 32 || bs == 64; }
 
 // A token stride in elements: rows of `width` elements that do not overlap,
@@ -33,7 +30,7 @@ pgd_status check_common(int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
                         bool *empty) {
     *empty = false;
     if (num_seqs < 0 || num_tokens < 0 || max_q_len < 0 || window < 0 || num_q_heads <= 0 ||
-        num_kv_heads <= 0 || num_ctas < 0 || num_ctas > kMaxCtas)
+        num_kv_heads <= 0 || num_ctas < 0 || num_ctas > kMaxPrefillCtas)
         return PGD_ERR_INVALID_ARG;
     if (num_q_heads % num_kv_heads) return PGD_ERR_INVALID_ARG;
     if (!std::isfinite(scale)) return PGD_ERR_INVALID_ARG;
@@ -48,8 +45,8 @@ pgd_status check_common(int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
 // Units are cut from this many keys on (the host's bound on a sequence's).
 constexpr int64_t kCutKeys = 1024;
 
-// Grid, and whether units are cut: one CTA per SM, at most one per unit where
-// they stay whole.  Cutting costs the merge kernel (about 4 us) and evens out
+// Grid, and whether units are cut: one CTA per SM, two per unit where they
+// stay whole.  Cutting costs the merge kernel (about 4 us) and evens out
 // what the longest unit would take alone (about 1 us per 128 keys).
 struct PrefillPlan {
     int grid;
@@ -66,16 +63,16 @@ PrefillPlan plan_prefill(int sms, int64_t num_seqs, int64_t num_tokens, int64_t 
     int64_t keys = max_keys > 0 ? max_keys : INT_MAX;
     if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + tpu);
     if (keys >= kCutKeys) return {sms, true};
-    return {static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, units))), false};
+    // twice the units: a share is then shorter than a unit, and no CTA gets two
+    return {static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, 2 * units))), false};
 }
 
 pgd_status run(PrefillLaunch &a, int64_t max_keys, int32_t num_ctas, void *workspace,
                size_t workspace_bytes, int64_t packed_rows, void *stream) {
     PrefillParams &p = a.p;
-    int sms = 0;
-    pgd_status st = device_info(&sms, &p.flags);
+    pgd_status st = device_info(&a.sms, &p.flags);
     if (st != PGD_OK) return st;
-    PrefillPlan plan = plan_prefill(sms, p.num_seqs, p.num_tokens, max_keys, p.window,
+    PrefillPlan plan = plan_prefill(a.sms, p.num_seqs, p.num_tokens, max_keys, p.window,
                                     p.num_q_heads, p.num_kv_heads, p.head_dim, num_ctas);
     if (plan.cut && workspace_bytes < prefill_workspace(plan.grid, p.head_dim)) {
         if (num_ctas > 0) return PGD_ERR_WORKSPACE;
