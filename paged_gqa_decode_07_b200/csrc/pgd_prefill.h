@@ -70,6 +70,6 @@ cudaError_t launch_kv_gather(const void *k_cache, const void *v_cache, const int
                              int32_t num_tokens, void *k_out, void *v_out, int32_t hkv,
                              int32_t head_dim, int32_t block_size, int64_t pool_slots, bool fp8,
                              const float *k_scale, const float *v_scale, uint32_t *flags,
-                             cudaStream_t stream);
+                             int sms, cudaStream_t stream);
 
 }  // namespace pgd

@@ -295,7 +295,7 @@ pgd_status pgd_kv_gather(const void *k_cache, const void *v_cache, const int64_t
     return launch_kv_gather(k_cache, v_cache, slot_mapping, num_tokens, k_out, v_out,
                             num_kv_heads, head_dim, block_size,
                             static_cast<int64_t>(num_blocks) * block_size, fp8, k_scale, v_scale,
-                            flags, static_cast<cudaStream_t>(stream)) == cudaSuccess
+                            flags, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PGD_OK
                : PGD_ERR_CUDA;
 }
