@@ -57,7 +57,6 @@ namespace pgd {
 
 constexpr uint32_t kLine = 128 * 128;         // bytes of a line: 128 rows x 128 B
 constexpr uint32_t kBox = 2 * kLine;          // [128 keys][128 dims], 16-bit
-constexpr uint32_t kRawBox = kLine;           // [128 keys][128 dims], 8-bit
 constexpr int kRedoSlots = 8;
 constexpr uint32_t kMetaBytes = 1024;
 
@@ -75,11 +74,9 @@ struct PrefillCfg {
     static constexpr int LINES = D / 64;              // lines of a Q tile
     static constexpr int BOXES = D / 128;             // boxes of a K or V tile
     static constexpr uint32_t QTILE = LINES * kLine;
-    static constexpr int NS = FP8 ? 3 : 5;            // ring of 16-bit boxes
-    static constexpr int NR = FP8 ? 4 : 0;            // ring of raw E4M3 boxes
+    static constexpr int NS = 5;                      // ring of boxes
     static constexpr uint32_t OFF_RING = NQ * QTILE;
-    static constexpr uint32_t OFF_RAW = OFF_RING + NS * kBox;
-    static constexpr uint32_t OFF_META = OFF_RAW + NR * kRawBox;
+    static constexpr uint32_t OFF_META = OFF_RING + NS * kBox;
     static constexpr uint32_t SMEM = OFF_META + kMetaBytes + (FP8 ? 2048 : 0);
     static_assert(SMEM <= 232448, "more shared memory than a CTA has");
 };
@@ -90,7 +87,6 @@ struct PrefillMeta {
     uint64_t q_full, q_ready, q_empty, drain, pv_done;
     uint64_t s_ready[2], p_ready[2][2], o_done[2];
     uint64_t full[5], empty[5], fixed[5];
-    uint64_t raw_full[4], raw_empty[4];
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     Piece piece[kPieces];
     Share share;
@@ -164,72 +160,82 @@ __device__ __forceinline__ bool clean_box(uint32_t box, int lo, int hi, int all_
     return bad;
 }
 
-// A raw E4M3 box to f16 (both with the 128-byte swizzle); as clean_box for
-// rows outside [lo, hi), which become zeros without being looked at.
+// An E4M3 box to f16, in place: a row's 128 bytes lie where the second half of
+// its 128 elements goes, and eight threads of one warp read the whole row
+// before they write it.  With `part`, as clean_box: rows outside [lo, hi)
+// become zeros unseen, and the others are looked at.
 template <int WARPS>
-__device__ __forceinline__ bool convert_box(uint32_t raw, uint32_t box, int lo, int hi, int tid) {
+__device__ __forceinline__ bool convert_box(uint32_t box, bool part, int lo, int hi, int tid) {
+    constexpr int U = 4;
     bool bad = false;
-#pragma unroll 4
-    for (int i = tid; i < 128 * 8; i += 32 * WARPS) {
-        const int r = i >> 3, c = i & 7, sw = r & 7;
-        uint32_t x[4];
-        lds128(raw + r * 128 + ((c ^ sw) << 4), x[0], x[1], x[2], x[3]);
-        if (r < lo || r >= hi) {
-            x[0] = x[1] = x[2] = x[3] = 0;
-        }
-        uint32_t y[8];
+    const int c = tid & 7, f = c >> 2, o = (c & 3) * 2;
+#pragma unroll 1
+    for (int r0 = tid >> 3; r0 < 128; r0 += U * WARPS * 4) {
+        uint32_t x[U][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            bad |= (((x[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-            y[2 * k] = e4m3x2_to_f16x2(x[k] & 0xFFFFu);
-            y[2 * k + 1] = e4m3x2_to_f16x2(x[k] >> 16);
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * WARPS * 4;
+            lds128(box + kLine + r * 128 + ((c ^ (r & 7)) << 4), x[u][0], x[u][1], x[u][2], x[u][3]);
         }
-        // 16 elements: two chunks of line c / 4; lanes of the second line
-        // write theirs in the other order, so that a row's eight lanes hit
-        // eight different chunk positions
-        const uint32_t row = box + (c >> 2) * kLine + r * 128;
-        const int o = (c & 3) * 2, f = c >> 2;
-        const uint32_t a0 = row + (((o + f) ^ sw) << 4), a1 = row + (((o + 1 - f) ^ sw) << 4);
-        if (f) {
-            sts128(a0, y[4], y[5], y[6], y[7]);
-            sts128(a1, y[0], y[1], y[2], y[3]);
-        } else {
-            sts128(a0, y[0], y[1], y[2], y[3]);
-            sts128(a1, y[4], y[5], y[6], y[7]);
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * WARPS * 4, sw = r & 7;
+            if (part) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (r < lo || r >= hi) x[u][k] = 0;
+                    bad |= (((x[u][k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+                }
+            }
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y[2 * k] = e4m3x2_to_f16x2(x[u][k] & 0xFFFFu);
+                y[2 * k + 1] = e4m3x2_to_f16x2(x[u][k] >> 16);
+            }
+            // 16 elements: two chunks of line c / 4; lanes of the second line
+            // write theirs in the other order, so that a row's eight lanes hit
+            // eight different chunk positions
+            const uint32_t row = box + f * kLine + r * 128;
+            const uint32_t a0 = row + (((o + f) ^ sw) << 4), a1 = row + (((o + 1 - f) ^ sw) << 4);
+            if (f) {
+                sts128(a0, y[4], y[5], y[6], y[7]);
+                sts128(a1, y[0], y[1], y[2], y[3]);
+            } else {
+                sts128(a0, y[0], y[1], y[2], y[3]);
+                sts128(a1, y[4], y[5], y[6], y[7]);
+            }
         }
     }
     return bad;
 }
 
-// A query row (one thread), bf16 -> f16 in place, multiplied by the power of
-// two that brings its largest element to [2^14, 2^15): exact for every element
-// within 2^-28 of it.  Returns the inverse power (1 for a row of zeros or
-// one that is not finite).
-__device__ __forceinline__ float convert_q_row(uint32_t tile, int r) {
-    const uint32_t sw = r & 7;
-    uint32_t m = 0;
-    for (int c = 0; c < 16; ++c) {
-        uint32_t x[4];
-        lds128(tile + (c >> 3) * kLine + r * 128 + (((c & 7) ^ sw) << 4), x[0], x[1], x[2], x[3]);
+// A query row (eight threads of one warp, two 16-byte chunks each), bf16 ->
+// f16 in place, multiplied by the power of two that brings its largest element
+// to [2^14, 2^15): exact for every element within 2^-28 of it.  Returns the
+// inverse power (1 for a row of zeros or one that is not finite).
+__device__ __forceinline__ float convert_q_row(uint32_t tile, int r, int c) {
+    const uint32_t a = tile + r * 128 + ((c ^ (r & 7)) << 4);
+    uint32_t x[8], m = 0;
+    lds128(a, x[0], x[1], x[2], x[3]);
+    lds128(a + kLine, x[4], x[5], x[6], x[7]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) m = __vmaxu2(m, x[k] & 0x7FFF7FFFu);
-    }
+    for (int k = 0; k < 8; ++k) m = __vmaxu2(m, x[k] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int off = 4; off; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
     const uint32_t top = max(m & 0xFFFFu, m >> 16);
     int e = static_cast<int>(top >> 7) - 127;            // floor(log2) of a normal
     if (top == 0 || top >= 0x7F80u) e = 14;
     if (e < -110) e = -110;                              // keep both powers normal
     const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-    for (int c = 0; c < 16; ++c) {
-        const uint32_t a = tile + (c >> 3) * kLine + r * 128 + (((c & 7) ^ sw) << 4);
-        uint32_t x[4];
-        lds128(a, x[0], x[1], x[2], x[3]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 f = unpack_bf16x2(x[k]);
-            x[k] = pack_f16x2(f.x * up, f.y * up);
-        }
-        sts128(a, x[0], x[1], x[2], x[3]);
+    for (int k = 0; k < 8; ++k) {
+        const float2 v = unpack_bf16x2(x[k]);
+        x[k] = pack_f16x2(v.x * up, v.y * up);
     }
+    sts128(a, x[0], x[1], x[2], x[3]);
+    sts128(a + kLine, x[4], x[5], x[6], x[7]);
     return __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
 }
 
@@ -274,7 +280,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
     }
     PrefillMeta &meta = *reinterpret_cast<PrefillMeta *>(smem_al + C::OFF_META);
     float *row_mult = reinterpret_cast<float *>(smem_al + C::OFF_META + kMetaBytes);
-    const uint32_t ring = smem + C::OFF_RING, raw_ring = smem + C::OFF_RAW;
+    const uint32_t ring = smem + C::OFF_RING;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const auto bar = [](uint64_t &b) { return smem_u32(&b); };
 
@@ -291,15 +297,11 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             mbar_init(bar(meta.o_done[i]), 1);
         }
         for (int i = 0; i < 5; ++i) {
-            // 16-bit ring: filled by TMA and read by the MMA and the V warps,
-            // or (FP8) filled by the V warps and read by the MMA
-            mbar_init(bar(meta.full[i]), FP8 ? C::V_WARPS : 1);
+            // filled by TMA; an FP8 box goes through the V warps before the
+            // MMA warp takes it, a bf16 box is looked at by both
+            mbar_init(bar(meta.full[i]), 1);
             mbar_init(bar(meta.empty[i]), FP8 ? 1 : 1 + C::V_WARPS);
             mbar_init(bar(meta.fixed[i]), C::V_WARPS);
-        }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(bar(meta.raw_full[i]), 1);
-            mbar_init(bar(meta.raw_empty[i]), C::V_WARPS);
         }
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(bar(meta.piece_full[i]), 1);
@@ -342,10 +344,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == 8) {
         // ================================================== producer
-        constexpr int N = FP8 ? C::NR : C::NS;
-        uint64_t *full = FP8 ? meta.raw_full : meta.full;
-        uint64_t *empty = FP8 ? meta.raw_empty : meta.empty;
-        const uint32_t base = FP8 ? raw_ring : ring;
+        constexpr int N = C::NS;
         const bool paged = p.block_table != nullptr;
         const int bs = p.block_size;
         const int nblk = paged ? kKeys / bs : 1;
@@ -380,10 +379,11 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             };
             const auto load = [&](const CUtensorMap *map, int j, int half, int id) {
                 const int s = boxes % N;
-                if (!wait(empty[s], ((boxes / N) & 1) ^ 1)) return false;
+                if (!wait(meta.empty[s], ((boxes / N) & 1) ^ 1)) return false;
                 ++boxes;
-                const uint32_t b = smem_u32(&full[s]);
-                const uint32_t dst = base + s * (FP8 ? kRawBox : kBox);
+                const uint32_t b = bar(meta.full[s]);
+                // E4M3 rows land where their second halves will be
+                const uint32_t dst = ring + s * kBox + (FP8 ? kLine : 0);
                 if (!paged) {
                     if (lane == 0) {
                         mbar_arrive_expect_tx(b, kBox);
@@ -443,7 +443,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         // every copy must land before the CTA exits
         bool landed = true;
         for (int i = max(0, boxes - N); i < boxes; ++i)
-            landed &= mbar_wait_bounded(smem_u32(&full[i % N]), (i / N) & 1, kDrainWaitNs);
+            landed &= mbar_wait_bounded(bar(meta.full[i % N]), (i / N) & 1, kDrainWaitNs);
         if (units > 0)
             landed &= mbar_wait_bounded(bar(meta.q_full), (units - 1) & 1, kDrainWaitNs);
         if (!landed) raise_flag(p.flags, kFlagTimeout);
@@ -478,12 +478,13 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                     mma_ts(tmem + d, a + kk * 8, b + kk * (2048 >> 4), kIdO, kk > 0 || acc);
             }
         };
+        uint64_t *ready = FP8 ? meta.fixed : meta.full;
         // the ring's next box; its slot is returned, -1 after a timeout
         const auto next_box = [&](bool fix) {
             const int s = slot;
-            const bool fixed = fix && !FP8;
-            const uint32_t parity = fixed ? (fixed_phase >> s) & 1 : phase;
-            if (fixed) fixed_phase ^= 1u << s;
+            const bool fixed = FP8 || fix;
+            const uint32_t parity = !FP8 && fix ? (fixed_phase >> s) & 1 : phase;
+            if (!FP8 && fix) fixed_phase ^= 1u << s;
             if (++slot == C::NS) {
                 slot = 0;
                 phase ^= 1;
@@ -519,14 +520,14 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                         const int sv = slot, sn = slot + 1 == C::NS ? 0 : slot + 1;
                         const uint32_t next_phase = phase ^ (slot + 1 == C::NS);
                         ok = false;
-                        if (!wait(meta.full[sv], phase)) break;
+                        if (!wait(ready[sv], phase)) break;
                         if (!wait(meta.p_ready[0][0], p_count & 1)) break;
                         tcgen05_fence_after();
                         pv(kOCol, 0, sv, 0, true);
                         if (!wait(meta.p_ready[0][1], p_count & 1)) break;
                         tcgen05_fence_after();
                         pv(kOCol, 0, sv, 1, true);
-                        if (!wait(meta.full[sn], next_phase)) break;
+                        if (!wait(ready[sn], next_phase)) break;
                         qk(0, 0, sn, 0);
                         if (leader) mma_commit(bar(meta.s_ready[0]));
                         if (!wait(meta.p_ready[1][0], p_count >> 1)) break;
@@ -639,10 +640,10 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             if (k.kb >= k.ke) continue;
             if (FP8) {
                 if (!(ok = wait(meta.q_full, units & 1))) break;
-                for (int r = tid; r < NQ * 128; r += 32 * C::V_WARPS) {
-                    if (r < 128 || k.t[NQ - 1].ntok > 0)
-                        row_mult[(units & 1) * 256 + r] =
-                            convert_q_row(smem + (r >> 7) * C::QTILE, r & 127);
+#pragma unroll 1
+                for (int r = tid >> 3; r < (k.t[NQ - 1].ntok > 0 ? NQ : 1) * 128; r += 4 * C::V_WARPS) {
+                    const float back = convert_q_row(smem + (r >> 7) * C::QTILE, r & 127, tid & 7);
+                    if ((tid & 7) == 0) row_mult[(units & 1) * 256 + r] = back;
                 }
                 fence_proxy_async();
                 __syncwarp();
@@ -656,27 +657,19 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                 const int j0 = j * kKeys;
                 const int lo = part ? k.lo - j0 : 0, hi = part ? k.hi - j0 : kKeys;
                 bool bad = false;
-                if (FP8) {
-                    const int r = box % (FP8 ? C::NR : 1);
-                    if (!wait(meta.raw_full[r], (box / (FP8 ? C::NR : 1)) & 1)) return false;
-                    if (!wait(meta.empty[s], ((box / C::NS) & 1) ^ 1)) return false;
-                    bad = convert_box<C::V_WARPS>(raw_ring + r * kRawBox, ring + s * kBox, lo, hi, tid);
+                if (!wait(meta.full[s], (box / C::NS) & 1)) return false;
+                if (FP8 || part) {
+                    if (FP8)
+                        bad = convert_box<C::V_WARPS>(ring + s * kBox, part, lo, hi, tid);
+                    else
+                        bad = clean_box<C::V_WARPS>(ring + s * kBox, lo, hi, k.all_lo - j0,
+                                                    k.all_hi - j0, tid);
                     fence_proxy_async();
-                    if (part && bad) meta.redo[units % kRedoSlots] = units;
+                    if (bad) meta.redo[units % kRedoSlots] = units;
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(meta.raw_empty[r]));
-                        mbar_arrive(bar(meta.full[s]));
-                    }
-                } else {
-                    if (!wait(meta.full[s], (box / C::NS) & 1)) return false;
-                    if (part) {
-                        bad = clean_box<C::V_WARPS>(ring + s * kBox, lo, hi, k.all_lo - j0, k.all_hi - j0, tid);
-                        fence_proxy_async();
-                        if (bad) meta.redo[units % kRedoSlots] = units;
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(meta.fixed[s]));
-                    }
+                    if (lane == 0) mbar_arrive(bar(meta.fixed[s]));
+                }
+                if (!FP8) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(meta.empty[s]));
                 }
