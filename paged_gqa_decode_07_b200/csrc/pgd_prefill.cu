@@ -11,13 +11,15 @@ namespace pgd {
 // at a time:
 //   out = sum_j exp(lse_j - M) o_j / sum_j exp(lse_j - M),  M = max_j lse_j
 // Latency bounds it: one round of loads for the list, and one for up to U
-// pieces of R rows, all issued before the first is used.
+// pieces of R rows, all issued before the first is used.  Two rows, two pieces
+// and 32 warps an SM were the best of R = 1 .. 4, U = 1 .. 4 and 16 .. 64
+// warps (a mixed step: 107 us in all, 112 with R = U = 4).
 constexpr int kMergeWarps = 16;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) prefill_merge_kernel(const PrefillParams p,
+__global__ void __launch_bounds__(32 * kMergeWarps, 2) prefill_merge_kernel(const PrefillParams p,
                                                                          int grid) {
-    constexpr int ROWS = D == 128 ? 256 : 128, E4 = D / 128, R = 4 / E4, U = 4;
+    constexpr int ROWS = D == 128 ? 256 : 128, E4 = D / 128, R = 2 / E4, U = 2;
     constexpr int T = 32 * kMergeWarps;
     // per boundary: the key tile that it cuts at, and whether the one before
     // lies inside the same unit; per unit: its first chunk, boundary and rows
@@ -194,7 +196,7 @@ static cudaError_t launch(const PrefillLaunch &a) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.sms);
+    cfg.gridDim = dim3(a.sms * 2);
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.stream = a.stream;
     cfg.attrs = attr;

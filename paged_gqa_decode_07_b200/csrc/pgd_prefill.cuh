@@ -11,8 +11,9 @@
 // diagonal is only 128 / g tokens wide.  A unit is NQ query tiles (2 at
 // head_dim 128, 1 at 256) and all keys that they see; keys come in tiles of 128.
 //
-// Work.  The units of all sequences laid end to end, each as long as its keys
-// plus a constant, are cut into one equal share per CTA (pgd_prefill_sched.cuh).
+// Work.  Long contexts: the units of all sequences laid end to end, each as
+// long as its keys plus a constant, are cut into one equal share per CTA
+// (pgd_prefill_sched.cuh; short ones deal whole units in turn).
 // A unit that a boundary cuts leaves one unrounded piece per CTA in the
 // workspace; a second kernel merges them by log-sum-exp.
 //
@@ -249,11 +250,9 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 
 // ---------------------------------------------------------------- the kernel
 // A warp's wait for a phase, all lanes or none: false when `limit_ns` ran out
-// (the timeout flag is raised).  A phase that is over costs 50 cycles; every
-// branch or 64-bit compare before the test showed (180 with four of them).
+// (the timeout flag is raised).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                           uint32_t *flags) {
-    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
     const uint32_t nap = limit_ns < 20000 ? static_cast<uint32_t>(limit_ns) : 20000u;
     uint64_t t0 = 0;
     while (!__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, nap))) {
@@ -265,6 +264,14 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
         }
     }
     return true;
+}
+
+// The same where a phase is often over: 50 cycles then, 100 by the form with a
+// time limit.
+__device__ __forceinline__ bool warp_wait_soon(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                               uint32_t *flags) {
+    return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) ||
+           warp_wait(bar, parity, limit_ns, flags);
 }
 
 template <int D, bool FP8>
@@ -314,7 +321,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         tma_prefetch_desc(&maps.v);
     }
     if (warp == 9) tmem_alloc(smem_u32(&meta.tmem), 512);
-    find_share<NQ, C::THREADS>(p, meta.share);               // meets at __syncthreads
+    if (p.parts) find_share<NQ, C::THREADS>(p, meta.share);   // all threads meet in it
     tcgen05_fence_before();
     __syncthreads();
     tcgen05_fence_after();
@@ -344,6 +351,9 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == 8) {
         // ================================================== producer
+        const auto wait = [&](uint64_t &b, uint32_t parity) {
+            return warp_wait_soon(smem_u32(&b), parity, limit, p.flags);
+        };
         constexpr int N = C::NS;
         const bool paged = p.block_table != nullptr;
         const int bs = p.block_size;
@@ -351,9 +361,10 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         int boxes = 0, units = 0;
         bool ok = true;
         PieceWalk<NQ> walk(p, meta.share);
+        UnitDeal<NQ> deal(p);
         while (ok) {
             Piece u;
-            const bool more = walk.next(u);
+            const bool more = p.parts ? walk.next(u) : deal.next(u);
             if (more) piece_keys<NQ>(p, u, tpq);
             else u.ntok = 0;
             if (!(ok = wait(meta.piece_empty[piece % kPieces], ((piece / kPieces) & 1) ^ 1))) break;
@@ -451,6 +462,9 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
         // ================================================== MMA issue
         constexpr uint32_t kIdS = mma_idesc(128, 128, !FP8, false);
         constexpr uint32_t kIdO = mma_idesc(128, 128, !FP8, true);
+        const auto wait = [&](uint64_t &b, uint32_t parity) {
+            return warp_wait_soon(smem_u32(&b), parity, limit, p.flags);
+        };
         const uint32_t leader = elect_one();
         int units = 0, steps = 0, slot = 0;
         uint32_t phase = 0, fixed_phase = 0;
@@ -737,13 +751,18 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                         for (int c = 0; c < 128; c += 32) {
                             if (!__any_sync(0xffffffffu, mult < 0.f || a < c + 32 || b > c)) continue;
                             float s[32];
-                            tmem_ld32(scol + c, s);
-                            tmem_wait_ld();
+                            if (!__any_sync(0xffffffffu, valid && a > c)) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                asm volatile("" : "+f"(s[i]));
-                                s[i] = mult < 0.f ? -s[i] : s[i];
-                                s[i] = c + i < a && c + i >= b ? s[i] : -INFINITY;
+                                for (int i = 0; i < 32; ++i) s[i] = -INFINITY;
+                            } else {
+                                tmem_ld32(scol + c, s);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    asm volatile("" : "+f"(s[i]));
+                                    s[i] = mult < 0.f ? -s[i] : s[i];
+                                    s[i] = c + i < a && c + i >= b ? s[i] : -INFINITY;
+                                }
                             }
                             tmem_st32(scol + c, s);
                         }

@@ -45,7 +45,7 @@ pgd_status check_common(int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
 // Units are cut from this many keys on (the host's bound on a sequence's).
 constexpr int64_t kCutKeys = 1024;
 
-// Grid, and whether units are cut: one CTA per SM, two per unit where they
+// Grid, and whether units are cut: one CTA per SM, one per unit where they
 // stay whole.  Cutting costs the merge kernel (about 4 us) and evens out
 // what the longest unit would take alone (about 1 us per 128 keys).
 struct PrefillPlan {
@@ -63,8 +63,7 @@ PrefillPlan plan_prefill(int sms, int64_t num_seqs, int64_t num_tokens, int64_t 
     int64_t keys = max_keys > 0 ? max_keys : INT_MAX;
     if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + tpu);
     if (keys >= kCutKeys) return {sms, true};
-    // twice the units: a share is then shorter than a unit, and no CTA gets two
-    return {static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, 2 * units))), false};
+    return {static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms, units))), false};
 }
 
 pgd_status run(PrefillLaunch &a, int64_t max_keys, int32_t num_ctas, void *workspace,
