@@ -253,9 +253,10 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // (the timeout flag is raised).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                           uint32_t *flags) {
-    const uint32_t nap = limit_ns < 20000 ? static_cast<uint32_t>(limit_ns) : 20000u;
+    // a try_wait may suspend the thread for a while; a shortened limit polls
+    const bool poll = limit_ns < kDefaultWaitNs;
     uint64_t t0 = 0;
-    while (!__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, nap))) {
+    while (!__all_sync(0xffffffffu, poll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) t0 = now;
         if (__any_sync(0xffffffffu, now - t0 > limit_ns)) {
@@ -266,8 +267,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_
     return true;
 }
 
-// The same where a phase is often over: 50 cycles then, 100 by the form with a
-// time limit.
+// The same where a phase is often over (50 cycles then).
 __device__ __forceinline__ bool warp_wait_soon(uint32_t bar, uint32_t parity, uint64_t limit_ns,
                                                uint32_t *flags) {
     return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) ||

@@ -80,16 +80,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r) {
         : "memory");
 }
 
-// try_wait that suspends the thread for about nap_ns at most.
-__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t nap_ns) {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok) : "r"(bar), "r"(parity), "r"(nap_ns) : "memory");
-    return ok != 0;
-}
-
 // ---------------------------------------------------------------- descriptors
 // Operands lie in shared memory as [line][row][128 bytes] with the 128-byte
 // swizzle (what the TMA loads write): a line holds 64 16-bit elements of the

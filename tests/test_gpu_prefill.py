@@ -534,3 +534,102 @@ def test_long_context_rows():
 def test_longer_prompts(hq, hkv, d):
     check_packed([2500, 1200], hq, hkv, d, seed=160, fused=True)
     check_packed([3333], hq, hkv, d, seed=161, window=700)
+
+
+def test_outputs_that_start_on_16_bytes():
+    """32-byte stores need more: such an output takes 16-byte ones."""
+    T, hq, hkv = 150, 8, 2
+    for d in (128, 256):
+        q, k, v = (randn((T, h, d), 170 + i) for i, h in enumerate((hq, hkv, hkv)))
+        cu, cu_t = cu_of([100, 50])
+        base = torch.full((T * hq * d + 16,), SENTINEL, dtype=torch.bfloat16, device="cuda")
+        out = base[8:8 + T * hq * d].view(T, hq, d)
+        assert out.data_ptr() % 32 == 16
+        for ctas in (0, 5):
+            pgd.prefill_attention(q, k, v, cu_t, hq, hkv, d, 0.09, out, num_ctas=ctas)
+            prefill_ref.assert_within(out, None, prefill_ref.packed(q, k, v, cu, 0, 0.09), 100, d,
+                                      "bf16", f"{ctas} CTAs")
+            assert bool((base[:8] == SENTINEL).all()) and bool((base[-8:] == SENTINEL).all())
+            out.fill_(0)
+
+
+@pytest.mark.parametrize("kw", [{"max_seq_len": 90}, {}, {"num_ctas": 1}, {"num_ctas": 97}],
+                         ids=["dealt", "cut", "one", "97"])
+@pytest.mark.parametrize("d", [128, 256])
+def test_more_sequences_than_a_cta_has_threads(d, kw):
+    g = torch.Generator().manual_seed(2)
+    lens = [int(x) for x in torch.randint(0, 7, (1300,), generator=g)]
+    lens[0] = lens[33] = lens[600] = lens[-1] = 0
+    lens[32], lens[511], lens[512], lens[1298] = 90, 40, 33, 77
+    check_packed(lens, 4, 2, d, seed=180, **kw)
+    check_packed([0] * 700 + [5], 2, 1, d, seed=181, **kw)
+    check_packed([0] * 700, 2, 1, d, seed=182, tail=2, **kw)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "e4m3"])
+def test_dealt_and_cut_work_agree_with_the_definition_in_pages(dt):
+    """Many short contexts: whole units dealt in turn (hints), or cut."""
+    g = torch.Generator().manual_seed(3)
+    ctx = [int(x) for x in torch.randint(1, 400, (60,), generator=g)]
+    q_lens = [min(n, int(x)) for n, x in zip(ctx, torch.randint(0, 30, (60,), generator=g))]
+    check_paged(q_lens, ctx, 8, 2, 128, 16, dt, seed=190)
+    check_paged(q_lens, ctx, 8, 2, 128, 16, dt, seed=190, num_ctas=33)
+
+
+def test_sequences_that_share_blocks():
+    """Two sequences over one prefix, and the same block twice in a table."""
+    hq, hkv, d, bs = 8, 2, 128, 16
+    kc, vc, table, _, _ = make_pages([200], hkv, d, bs, "bf16", 200)
+    table = torch.cat([table, table])
+    table[1, 3] = table[1, 2]
+    cu, cu_t = cu_of([40, 25])
+    q = randn((65, hq, d), 201)
+    ctx = [200, 180]
+    out, lse = run_paged(q, kc, vc, table, ctx, cu_t, hq, hkv, d, bs, 0.09, None, None)
+    ref = prefill_ref.paged(q, kc, vc, table, ctx, cu, 0, 0.09)
+    prefill_ref.assert_within(out, lse, ref, 200, d, "bf16")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "e4m3"])
+def test_blocks_past_32_bit_offsets(dt):
+    """A pool whose last blocks start past 2^32 bytes."""
+    hq, hkv, d, bs = 4, 2, 128, 64
+    nb = 140000 if dt == "bf16" else 270000
+    shape, kind = (nb, hkv, bs, d), torch.bfloat16 if dt == "bf16" else torch.uint8
+    small = make_pages([300], hkv, d, bs, dt, 210, extra=0)
+    kc, vc = (torch.empty(shape, dtype=kind, device="cuda") for _ in range(2))
+    need = small[0].shape[0]
+    assert (nb - need) * hkv * bs * d * kc.element_size() > 1 << 32
+    kc[nb - need:], vc[nb - need:] = small[0], small[1]
+    table = torch.where(small[2] < need, small[2] + (nb - need), small[2])
+    cu, cu_t = cu_of([70])
+    q = randn((70, hq, d), 211)
+    out, lse = run_paged(q, kc, vc, table, [300], cu_t, hq, hkv, d, bs, 0.09, small[3], small[4])
+    ref = prefill_ref.paged(q, fp8(small[0]), fp8(small[1]), small[2], [300], cu, 0, 0.09, small[3],
+                            small[4])
+    prefill_ref.assert_within(out, lse, ref, 300, d, dt)
+    # the same rows read back
+    pos = torch.arange(300, device="cuda")
+    slots = table[0, pos // bs].long() * bs + pos % bs
+    ko, _ = pgd.kv_gather(kc, vc, slots, k_scale=small[3], v_scale=small[4])
+    want = prefill_ref.pages(fp8(small[0]), small[2][0], 300, small[3])
+    assert bool(((ko.double() - want).abs() <= want.abs() * 2.0 ** -8).all())
+
+
+def test_scores_that_overflow_stay_in_their_rows():
+    """A finite query and key whose product is +inf: that row is not finite,
+    the others are as if the key were any other."""
+    T, hq, hkv, d = 300, 4, 1, 128
+    q, k, v = (randn((T, h, d), 220 + i) for i, h in enumerate((hq, hkv, hkv)))
+    k[40, 0, :], q[200, 1, :] = 0, 0
+    k[40, 0, 7], q[200, 1, 7] = 1e38, 1e38
+    q[:, :, 7][torch.arange(T, device="cuda") != 200] = 0
+    q[200, [0, 2, 3], 7] = 0
+    ref = prefill_ref.packed(q, k, v, [0, T], 0, 0.09)
+    cu, cu_t = cu_of([T])
+    for ctas in (0, 3):
+        out, lse = run_packed(q, k, v, cu_t, hq, hkv, d, 0.09, num_ctas=ctas)
+        keep = torch.ones((T, hq), dtype=torch.bool, device="cuda")
+        keep[200, 1] = False
+        prefill_ref.assert_within(out[keep], lse[keep], [r[keep] for r in ref], T, d, "bf16")
+        assert not bool(torch.isfinite(out[200, 1]).any())

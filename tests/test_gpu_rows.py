@@ -34,7 +34,7 @@ def want_scale(x):
     return (m / 448).float().clamp_min(2.0 ** -40)
 
 
-@pytest.mark.parametrize("n", [0, 1, 2, 7, 200, 5000])
+@pytest.mark.parametrize("n", [0, 1, 2, 7, 200, 256, 257, 5000])
 @pytest.mark.parametrize("hkv,d", [(1, 128), (2, 128), (3, 128), (8, 128), (1, 256), (5, 256),
                                    (8, 256), (40, 128), (33, 256)])
 def test_scales(n, hkv, d):
@@ -152,3 +152,44 @@ def test_row_operators_capture_and_prepare():
     call()
     torch.cuda.synchronize()
     assert torch.equal(ks, want_scale(k)) and torch.equal(vs, want_scale(v))
+
+
+def test_accumulate_with_few_and_with_many_rows():
+    """Both forms of the kernel raise the scales that the other wrote."""
+    a, b = randn((256, 3, 128), 11), randn((900, 3, 128), 12)
+    a[:, 1] *= 7
+    for x, y in ((a, b), (b, a)):
+        ks, vs = pgd.kv_quant_scales(x, -x)
+        pgd.kv_quant_scales(y, -y, ks, vs, accumulate=True)
+        both = want_scale(torch.cat([a, b]))
+        assert torch.equal(ks, both) and torch.equal(vs, both)
+
+
+@pytest.mark.parametrize("hkv,d,bs,dt", [
+    (1, 128, 16, "bf16"), (1, 128, 16, "e4m3"), (3, 256, 32, "e4m3"), (40, 128, 16, "bf16")])
+@pytest.mark.parametrize("shift", [0, 8])
+def test_gather_of_many_rows(hkv, d, bs, dt, shift):
+    """Several tokens a CTA, the last CTA not full, padding and slots past the
+    pool among them, outputs on 32 and on 16 bytes."""
+    nb, n = 53, 5003
+    k, v = pool(nb, hkv, bs, d, dt, 4), pool(nb, hkv, bs, d, dt, 5)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    slots = torch.randint(-40, nb * bs, (n,), generator=g, device="cuda")
+    slots[100], slots[4999] = nb * bs, 1 << 41
+    ks, vs = (torch.exp2(torch.randn(hkv, generator=g, device="cuda")) for _ in range(2))
+    base = [torch.full((n * hkv * d + 16,), -7.25, dtype=torch.bfloat16, device="cuda")
+            for _ in range(2)]
+    ko, vo = (x[shift:shift + n * hkv * d].view(n, hkv, d) for x in base)
+    pgd.kv_gather(k, v, slots, ko, vo, k_scale=ks, v_scale=vs)
+    assert pgd.get_device_error() == 4
+    on = (slots >= 0) & (slots < nb * bs)
+    at = torch.where(on, slots, 0)
+    for out, cache, sc, x in ((ko, k, ks, base[0]), (vo, v, vs, base[1])):
+        rows = cache.transpose(1, 2).reshape(nb * bs, hkv, d)[at]
+        if dt == "e4m3":
+            rows = (rows.view(torch.float8_e4m3fn).float() * sc[:, None]).to(torch.bfloat16)
+            same = (out == rows) | (torch.isnan(out) & torch.isnan(rows))
+        else:
+            same = out.view(torch.int16) == rows.view(torch.int16)
+        assert bool(same[on].all()) and bool((out[~on] == -7.25).all())
+        assert bool((x[:shift] == -7.25).all()) and bool((x[shift + n * hkv * d:] == -7.25).all())
