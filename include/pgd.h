@@ -302,7 +302,7 @@ pgd_status pgd_paged_decode_attention_ex(
  *                [0, num_tokens]; a sequence that breaks this flags
  *                PGD_ERR_DEVICE_BOUNDS and is skipped
  *   num_tokens   rows that q, k, v, out and lse_out hold; rows that belong to
- *                no sequence are neither read nor written
+ *                no sequence are not written and have no influence
  *   max_seq_len  host hint >= every length (0 = unknown); only used to choose
  *                whether work is cut
  *   window       0 = the whole causal range; > 0 = the last `window` positions

@@ -738,7 +738,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                         if (FP8) mult *= __ldg(p.k_scale + u.h) * row_mult[((units - 1) & 1) * 256 + t * 128 + r];
                         // a scale of zero: every visible key weighs the same,
                         // and masked scores (-inf) must still vanish
-                        if (mult == 0.f) mult = 0x1p-126f;
+                        if (mult == 0.f) mult = 0x1p-149f;
                     }
                     const bool masked = j < tk.mlo || j >= tk.mhi;
                     if (__any_sync(0xffffffffu, masked || mult < 0.f)) {

@@ -62,6 +62,7 @@ __device__ __forceinline__ SeqRows seq_rows(const PrefillParams &p, int s, bool 
     if (s >= p.num_seqs) return r;
     const int a = __ldg(p.cu + s), b = __ldg(p.cu + s + 1);
     int n = p.block_table ? __ldg(p.context_lens + s) : 0;
+    if (a == b && a >= 0 && b <= p.num_tokens) return r;       // no rows: no context either
     if (a < 0 || b < a || b > p.num_tokens) {
         if (report) raise_flag(p.flags, kFlagContextLen);
         return r;

@@ -633,3 +633,25 @@ def test_scores_that_overflow_stay_in_their_rows():
         keep[200, 1] = False
         prefill_ref.assert_within(out[keep], lse[keep], [r[keep] for r in ref], T, d, "bf16")
         assert not bool(torch.isfinite(out[200, 1]).any())
+
+
+def test_contexts_of_sequences_without_rows_are_not_looked_at():
+    """A padded batch: no query rows, any context length."""
+    kc, vc, table, _, _ = make_pages([60, 60, 60], 2, 128, 16, "bf16", 230)
+    cu, cu_t = cu_of([20, 0, 0])
+    q = randn((20, 4, 128), 231)
+    for kw in ({}, {"max_context_len": 64}):
+        out, lse = run_paged(q, kc, vc, table, [60, -5, 1 << 30], cu_t, 4, 2, 128, 16, 0.09, None,
+                             None, **kw)
+        assert pgd.get_device_error() == 0
+        ref = prefill_ref.paged(q, kc, vc, table, [60, 0, 0], cu, 0, 0.09)
+        prefill_ref.assert_within(out, lse, ref, 60, 128, "bf16")
+
+
+def test_a_scale_of_zero_weighs_large_scores_alike():
+    q, k, v = (randn((140, h, 128), 240 + i) for i, h in enumerate((4, 2, 2)))
+    q, k = q * 1e15, k * 1e15          # scores of up to 1e32
+    cu, cu_t = cu_of([140])
+    out, lse = run_packed(q, k, v, cu_t, 4, 2, 128, 0.0)
+    ref = prefill_ref.packed(q, k, v, cu, 0, 0.0)
+    prefill_ref.assert_within(out, lse, ref, 140, 128, "bf16")
