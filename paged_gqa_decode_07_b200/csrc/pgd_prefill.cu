@@ -10,22 +10,22 @@ namespace pgd {
 // units from the records, and the units' query rows are dealt to all warps, R
 // at a time:
 //   out = sum_j exp(lse_j - M) o_j / sum_j exp(lse_j - M),  M = max_j lse_j
-// Latency bounds it: one round of loads for the list, and one for up to U
-// pieces of R rows, all issued before the first is used.  Two rows, two pieces
-// and 32 warps an SM were the best of R = 1 .. 4, U = 1 .. 4 and 16 .. 64
-// warps (a mixed step: 107 us in all, 112 with R = U = 4).
+// Instruction issue bounded the first forms (a warp's lanes all computed every
+// row's weights and addresses: 300 instructions a row, 0.7 of the issue slots,
+// 12 us behind a mixed step); here lane r * PB + j has row r's weight of piece
+// j, and all lanes load and add 16 bytes of each row.
 constexpr int kMergeWarps = 16;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps, 2) prefill_merge_kernel(const PrefillParams p,
                                                                          int grid) {
-    constexpr int ROWS = D == 128 ? 256 : 128, E4 = D / 128, R = 2 / E4, U = 2;
+    constexpr int ROWS = D == 128 ? 256 : 128, E4 = D / 128, R = D == 128 ? 4 : 1, PB = 32 / R;
     constexpr int T = 32 * kMergeWarps;
     // per boundary: the key tile that it cuts at, and whether the one before
     // lies inside the same unit; per unit: its first chunk, boundary and rows
     __shared__ int cut_at[kMaxPrefillCtas + 1];
     __shared__ int first_chunk[kMaxPrefillCtas];
-    __shared__ short first_cta[kMaxPrefillCtas];
+    __shared__ short first_cta[kMaxPrefillCtas], pieces_of[kMaxPrefillCtas];
     __shared__ int4 rows_of[kMaxPrefillCtas];       // row0, ntok, h, tiles
     __shared__ int warp_units[kMergeWarps], warp_chunks[kMergeWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -74,7 +74,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) prefill_merge_kernel(cons
         if (x <= grid) cut_at[x] = head ? -q0.z : q0.z > 0 ? q0.z : 0;
     }
     __syncthreads();
-    const int tpq = 128 / p.group;
+    for (int u = threadIdx.x; u < units; u += T) {
+        int x = first_cta[u] + 1;
+        while (cut_at[x] > 0) ++x;                 // cut_at[grid] is no continuation
+        pieces_of[u] = static_cast<short>(x - first_cta[u] + 1);
+    }
+    __syncthreads();
+    const int tpq = 128 / p.group, r = lane / PB, q = lane % PB;
     for (int chunk = blockIdx.x * kMergeWarps + warp; chunk < chunks;
          chunk += gridDim.x * kMergeWarps) {
         int a = 0, b = units;                      // the unit of this chunk
@@ -83,95 +89,90 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) prefill_merge_kernel(cons
             if (first_chunk[mid] <= chunk) a = mid;
             else b = mid;
         }
-        const int c = first_cta[a], i0 = (chunk - first_chunk[a]) * R;
+        const int c = first_cta[a], count = pieces_of[a];
         const int4 unit = rows_of[a];
-        const int n = unit.y * p.group;
-        int row[R];
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-            const int i = i0 + q, tok = i / p.group;
-            row[q] = i < n ? tok / tpq * 128 + (tok % tpq) * p.group + (i - tok * p.group) : -1;
-        }
-        float m[R], l[R];
+        // the lane's row: of the workspace's slots, and of the output
+        const int i = (chunk - first_chunk[a]) * R + r, tok = i / p.group, hd = i - tok * p.group;
+        const bool on = i < unit.y * p.group;
+        const int tile = tok / tpq, row = tile * 128 + (tok - tile * tpq) * p.group + hd;
+        const int64_t orow = static_cast<int64_t>(unit.x + tok) * p.num_q_heads + unit.z * p.group + hd;
+        float m = -INFINITY, l = 0.f;
         float4 acc[R][E4];
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-            m[q] = -INFINITY;
-            l[q] = 0.f;
+        for (int k = 0; k < R * E4; ++k) acc[k / E4][k % E4] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j0 = 0; j0 < count; j0 += PB) {
+            // piece j: the first ends at the head's cut, the others start at
+            // CTA c + j - 1's and end at the next one's, the last with the unit
+            const int j = j0 + q;
+            const int start = j == 0 || j >= count ? 0 : j == 1 ? -cut_at[c] : cut_at[c + j - 1];
+            const int end = j >= count ? 0 : j + 1 == count ? unit.w : j == 0 ? -cut_at[c] : cut_at[c + j];
+            const int slot = j == 0 ? 2 * (c - 1) + 1 : 2 * (c + j - 1);
+            const bool live = end > start;
+            const float lse = live && on ? p.lse_part[static_cast<int64_t>(slot) * ROWS + row] : -INFINITY;
+            float top = lse;
 #pragma unroll
-            for (int k = 0; k < E4; ++k) acc[q][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        int start = 0, slot = 2 * (c - 1) + 1, x = c;  // the next piece: [start, cut of x)
-        bool more = true;
-        while (more) {
-            float lse[U][R];
-            float4 o[U][R][E4];
+            for (int off = PB / 2; off; off >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            top = fmaxf(top, m);
+            const float old = m == -INFINITY ? 0.f : expf(m - top);
+            // a NaN or +inf moves no maximum and stays in the sums
+            const float w = lse == -INFINITY ? 0.f : expf(lse - top);
+            m = top;
+            float sum = w;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                // the head's cut ends the first piece, a continuation's the others
-                const int mark = x == c ? -cut_at[x] : cut_at[x];
-                const int end = mark > 0 ? mark : unit.w;
-                const bool live = more && end > start;
+            for (int off = PB / 2; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            l = l * old + sum;
+            if (j0 > 0) {
 #pragma unroll
-                for (int q = 0; q < R; ++q) {
-                    lse[u][q] = -INFINITY;
-                    if (live && row[q] >= 0) {
-                        const int64_t pr = static_cast<int64_t>(slot) * ROWS + row[q];
-                        lse[u][q] = p.lse_part[pr];
-#pragma unroll
-                        for (int k = 0; k < E4; ++k)
-                            o[u][q][k] = *reinterpret_cast<const float4 *>(
-                                p.o_part + pr * D + k * 128 + lane * 4);
-                    }
-                }
-                if (mark <= 0) more = false;
-                if (more) {
-                    start = end;
-                    slot = 2 * x;
-                    ++x;
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < R; ++q) {
-                float top = m[q];
-#pragma unroll
-                for (int u = 0; u < U; ++u) top = fmaxf(top, lse[u][q]);
-                const float old = m[q] == -INFINITY ? 0.f : expf(m[q] - top);
-                m[q] = top;
-                l[q] *= old;
-#pragma unroll
-                for (int k = 0; k < E4; ++k) {
-                    acc[q][k].x *= old; acc[q][k].y *= old; acc[q][k].z *= old; acc[q][k].w *= old;
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    // a NaN or +inf moves no maximum and stays in the sums
-                    if (lse[u][q] == -INFINITY) continue;
-                    const float w = expf(lse[u][q] - top);
-                    l[q] += w;
+                for (int z = 0; z < R; ++z) {
+                    const float f = __shfl_sync(0xffffffffu, old, z * PB);
 #pragma unroll
                     for (int k = 0; k < E4; ++k) {
-                        acc[q][k].x += w * o[u][q][k].x; acc[q][k].y += w * o[u][q][k].y;
-                        acc[q][k].z += w * o[u][q][k].z; acc[q][k].w += w * o[u][q][k].w;
+                        acc[z][k].x *= f; acc[z][k].y *= f; acc[z][k].z *= f; acc[z][k].w *= f;
+                    }
+                }
+            }
+            unsigned left = __ballot_sync(0xffffffffu, live) & ((1u << PB) - 1);
+            while (left) {
+                const int at = __ffs(left) - 1;
+                left &= left - 1;
+                const float *src = p.o_part +
+                    static_cast<int64_t>(__shfl_sync(0xffffffffu, slot, at)) * (ROWS * D) + lane * 4;
+                float4 o[R][E4];
+#pragma unroll
+                for (int z = 0; z < R; ++z) {
+                    const int rz = __shfl_sync(0xffffffffu, on ? row : -1, z * PB);
+#pragma unroll
+                    for (int k = 0; k < E4; ++k) {
+                        o[z][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (rz >= 0) o[z][k] = *reinterpret_cast<const float4 *>(src + rz * D + k * 128);
+                    }
+                }
+#pragma unroll
+                for (int z = 0; z < R; ++z) {
+                    const float f = __shfl_sync(0xffffffffu, w, z * PB + at);
+                    if (f == 0.f) continue;
+#pragma unroll
+                    for (int k = 0; k < E4; ++k) {
+                        acc[z][k].x += f * o[z][k].x; acc[z][k].y += f * o[z][k].y;
+                        acc[z][k].z += f * o[z][k].z; acc[z][k].w += f * o[z][k].w;
                     }
                 }
             }
         }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-        for (int q = 0; q < R; ++q) {
-            if (row[q] < 0) continue;
-            const float inv = l[q] == 0.f ? 0.f : 1.f / l[q];
-            const int i = i0 + q, tok = i / p.group;
-            const int64_t orow = static_cast<int64_t>(unit.x + tok) * p.num_q_heads +
-                                 unit.z * p.group + (i - tok * p.group);
+        for (int z = 0; z < R; ++z) {
+            const float f = __shfl_sync(0xffffffffu, inv, z * PB);
+            const int64_t to = __shfl_sync(0xffffffffu, on ? orow : -1ll, z * PB);
+            if (to < 0) continue;
 #pragma unroll
             for (int k = 0; k < E4; ++k)
-                *reinterpret_cast<uint2 *>(p.out + orow * D + k * 128 + lane * 4) =
-                    make_uint2(pack_bf16x2(acc[q][k].x * inv, acc[q][k].y * inv),
-                               pack_bf16x2(acc[q][k].z * inv, acc[q][k].w * inv));
-            if (p.lse_out && lane == 0)
-                p.lse_out[orow] = l[q] == 0.f ? -INFINITY : m[q] + logf(l[q]);
+                *reinterpret_cast<uint2 *>(p.out + to * D + k * 128 + lane * 4) =
+                    make_uint2(pack_bf16x2(acc[z][k].x * f, acc[z][k].y * f),
+                               pack_bf16x2(acc[z][k].z * f, acc[z][k].w * f));
         }
+        if (p.lse_out && on && q == 0) p.lse_out[orow] = l == 0.f ? -INFINITY : m + logf(l);
     }
 }
 
