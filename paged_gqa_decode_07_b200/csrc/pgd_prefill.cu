@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) prefill_merge_kernel(cons
                     }
                 }
             }
-            unsigned left = __ballot_sync(0xffffffffu, live) & ((1u << PB) - 1);
+            unsigned left = __ballot_sync(0xffffffffu, live) & (0xffffffffu >> (32 - PB));
             while (left) {
                 const int at = __ffs(left) - 1;
                 left &= left - 1;
