@@ -13,6 +13,7 @@ the same C call (same buffers, sizes and stream) each time it is called.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -590,6 +591,13 @@ def _prefill_workspace(workspace, need: int, device, stream):
     return ws, need
 
 
+@functools.lru_cache(maxsize=256)
+def _prefill_need(device: int, *sizes: int) -> int:
+    """pgd_prefill_workspace_bytes on the current device (a function of the
+    sizes and the device alone)."""
+    return int(load_library().pgd_prefill_workspace_bytes(*sizes))
+
+
 def prefill_workspace_bytes(num_seqs: int, num_tokens: int, max_context_len: int, window: int,
                             num_q_heads: int, num_kv_heads: int, head_dim: int,
                             num_ctas: int = 0) -> int:
@@ -630,8 +638,9 @@ def prefill_attention(q, k, v, cu_seqlens, num_q_heads: int, num_kv_heads: int, 
             lse_out is not None and tuple(lse_out.shape) != (T, num_q_heads)):
         raise ValueError("prefill_attention: output shapes")
     _same_device("prefill_attention", q, k, v, cu_seqlens, out, lse_out, workspace)
-    need = prefill_workspace_bytes(B, T, min(max_seq_len or T, T), window, num_q_heads,
-                                   num_kv_heads, head_dim, num_ctas) if workspace is None else 0
+    need = 0 if workspace is not None else _prefill_need(
+        q.device.index, B, T, min(max_seq_len or T, T), window, num_q_heads, num_kv_heads,
+        head_dim, num_ctas)
     ws, ws_bytes = _prefill_workspace(workspace, need, q.device, stream)
     return _issue(lib.pgd_prefill_attention, "pgd_prefill_attention", (
         _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(cu_seqlens), B, T, int(max_seq_len),
@@ -684,8 +693,9 @@ def paged_prefill_attention(q, k_cache, v_cache, block_table, context_lens, cu_s
     _same_device("paged_prefill_attention", q, k_cache, v_cache, block_table, context_lens,
                  cu_seqlens, k_scale, v_scale, out, lse_out, workspace)
     cap = block_table.shape[1] * block_size
-    need = prefill_workspace_bytes(B, T, min(max_context_len or cap, cap), window,
-                                   num_q_heads, num_kv_heads, head_dim, num_ctas) if workspace is None else 0
+    need = 0 if workspace is not None else _prefill_need(
+        q.device.index, B, T, min(max_context_len or cap, cap), window, num_q_heads, num_kv_heads,
+        head_dim, num_ctas)
     ws, ws_bytes = _prefill_workspace(workspace, need, q.device, stream)
     return _issue(lib.pgd_paged_prefill_attention, "pgd_paged_prefill_attention", (
         _ptr(q), qs, _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
