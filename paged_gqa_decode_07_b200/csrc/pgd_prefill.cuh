@@ -45,6 +45,15 @@
 // the rest; where there is one, the unit's rows are computed again one warp
 // per row from the definition (attend_row), which touches visible keys only.
 //
+// What bounds it (148 SMs).  A step of two tiles takes the tensor cores 2048
+// cycles and ex2 2048, and one tile's chain (softmax 2000 - 2400, products
+// 1330) leaves both busy 0.55 - 0.6 of the time.  64 heads over 8, 8192 tokens:
+// 980 - 1040 us, 1.06 - 1.12 PFLOP/s at the power cap (992 W, 1.74 GHz), where
+// plain matrix products sustain 1.39.  Every instruction of the MMA warp
+// counts: descriptors built per product (18 instructions each), branches and
+// 64-bit compares before a wait and conditions in the loop cost 5400 cycles a
+// step, the straight form 3700.
+//
 // Every wait is bounded (wait_ns): a role that gives up raises the timeout
 // flag and leaves; the producer and the MMA warp then wait for what they have
 // in flight, all warps meet, and tensor memory is freed.
@@ -348,606 +357,609 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
     };
 
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
-    if (warp == 8) {
-        // ================================================== producer
-        const auto wait = [&](uint64_t &b, uint32_t parity) {
-            return warp_wait_soon(smem_u32(&b), parity, limit, p.flags);
-        };
-        constexpr int N = C::NS;
-        const bool paged = p.block_table != nullptr;
-        const int bs = p.block_size;
-        const int nblk = paged ? kKeys / bs : 1;
-        int boxes = 0, units = 0;
-        bool ok = true;
-        PieceWalk<NQ> walk(p, meta.share);
-        UnitDeal<NQ> deal(p);
-        while (ok) {
-            Piece u;
-            const bool more = p.parts ? walk.next(u) : deal.next(u);
-            if (more) piece_keys<NQ>(p, u, tpq);
-            else u.ntok = 0;
-            if (!(ok = wait(meta.piece_empty[piece % kPieces], ((piece / kPieces) & 1) ^ 1))) break;
-            if (lane == 0) {
-                meta.piece[piece % kPieces] = u;
-                mbar_arrive(bar(meta.piece_full[piece % kPieces]));
-            }
-            ++piece;
-            if (!more) break;
-            if (u.kb >= u.ke) continue;
-            const int32_t *table = p.block_table + static_cast<int64_t>(u.seq) * p.max_blocks_per_seq;
-            // block ids of key tile j: lane b % nblk holds block b's (or -1)
-            const auto ids = [&](int j) {
-                if (!paged || j >= u.ke) return -1;
-                const int key = j * kKeys + (lane % nblk) * bs;
-                if (key + bs <= u.lo || key >= u.hi) return -1;
-                int id = __ldg(table + key / bs);
-                if (id < 0 || id >= p.num_blocks) {
-                    raise_flag(p.flags, kFlagBlockId);
-                    id = 0;
-                }
-                return id;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
+        if (warp == 8) {
+            // ================================================== producer
+            const auto wait = [&](uint64_t &b, uint32_t parity) {
+                return warp_wait_soon(smem_u32(&b), parity, limit, p.flags);
             };
-            const auto load = [&](const CUtensorMap *map, int j, int half, int id) {
-                const int s = boxes % N;
-                if (!wait(meta.empty[s], ((boxes / N) & 1) ^ 1)) return false;
-                ++boxes;
-                const uint32_t b = bar(meta.full[s]);
-                // E4M3 rows land where their second halves will be
-                const uint32_t dst = ring + s * kBox + (FP8 ? kLine : 0);
-                if (!paged) {
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(b, kBox);
+            constexpr int N = C::NS;
+            const bool paged = p.block_table != nullptr;
+            const int bs = p.block_size;
+            const int nblk = paged ? kKeys / bs : 1;
+            int boxes = 0, units = 0;
+            bool ok = true;
+            PieceWalk<NQ> walk(p, meta.share);
+            UnitDeal<NQ> deal(p);
+            while (ok) {
+                Piece u;
+                const bool more = p.parts ? walk.next(u) : deal.next(u);
+                if (more) piece_keys<NQ>(p, u, tpq);
+                else u.ntok = 0;
+                if (!(ok = wait(meta.piece_empty[piece % kPieces], ((piece / kPieces) & 1) ^ 1))) break;
+                if (lane == 0) {
+                    meta.piece[piece % kPieces] = u;
+                    mbar_arrive(bar(meta.piece_full[piece % kPieces]));
+                }
+                ++piece;
+                if (!more) break;
+                if (u.kb >= u.ke) continue;
+                const int32_t *table = p.block_table + static_cast<int64_t>(u.seq) * p.max_blocks_per_seq;
+                // block ids of key tile j: lane b % nblk holds block b's (or -1)
+                const auto ids = [&](int j) {
+                    if (!paged || j >= u.ke) return -1;
+                    const int key = j * kKeys + (lane % nblk) * bs;
+                    if (key + bs <= u.lo || key >= u.hi) return -1;
+                    int id = __ldg(table + key / bs);
+                    if (id < 0 || id >= p.num_blocks) {
+                        raise_flag(p.flags, kFlagBlockId);
+                        id = 0;
+                    }
+                    return id;
+                };
+                const auto load = [&](const CUtensorMap *map, int j, int half, int id) {
+                    const int s = boxes % N;
+                    if (!wait(meta.empty[s], ((boxes / N) & 1) ^ 1)) return false;
+                    ++boxes;
+                    const uint32_t b = bar(meta.full[s]);
+                    // E4M3 rows land where their second halves will be
+                    const uint32_t dst = ring + s * kBox + (FP8 ? kLine : 0);
+                    if (!paged) {
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(b, kBox);
 #pragma unroll
-                        for (int l = 0; l < 2; ++l)
-                            tma_load_3d(dst + l * kLine, map, b, (2 * half + l) * 64, u.h,
-                                        u.kv0 + j * kKeys);
+                            for (int l = 0; l < 2; ++l)
+                                tma_load_3d(dst + l * kLine, map, b, (2 * half + l) * 64, u.h,
+                                            u.kv0 + j * kKeys);
+                        }
+                    } else {
+                        constexpr int L = FP8 ? 1 : 2;       // loads per block
+                        const bool mine = lane < nblk * L && id >= 0;
+                        const int cnt = __popc(__ballot_sync(0xffffffffu, mine));
+                        if (lane == 0) mbar_arrive_expect_tx(b, cnt * bs * 128);
+                        __syncwarp();
+                        if (mine) {
+                            const int l = lane / nblk;
+                            tma_load_4d(dst + l * kLine + (lane % nblk) * bs * 128, map, b, 0, 0,
+                                        FP8 ? 0 : 2 * half + l, id * p.num_kv_heads + u.h);
+                        }
                     }
-                } else {
-                    constexpr int L = FP8 ? 1 : 2;       // loads per block
-                    const bool mine = lane < nblk * L && id >= 0;
-                    const int cnt = __popc(__ballot_sync(0xffffffffu, mine));
-                    if (lane == 0) mbar_arrive_expect_tx(b, cnt * bs * 128);
                     __syncwarp();
-                    if (mine) {
-                        const int l = lane / nblk;
-                        tma_load_4d(dst + l * kLine + (lane % nblk) * bs * 128, map, b, 0, 0,
-                                    FP8 ? 0 : 2 * half + l, id * p.num_kv_heads + u.h);
-                    }
+                    return true;
+                };
+                int id = ids(u.kb), id_next = ids(u.kb + 1);
+                if (!(ok = wait(meta.q_empty, (units & 1) ^ 1))) break;
+                ++units;
+                if (lane == 0) {
+                    const uint32_t b = bar(meta.q_full);
+                    int tiles = 0;
+                    for (int i = 0; i < NQ; ++i) tiles += u.t[i].ntok > 0;
+                    mbar_arrive_expect_tx(b, tiles * C::LINES * tpq * p.group * 128);
+                    for (int i = 0; i < tiles; ++i)
+                        for (int l = 0; l < C::LINES; ++l)
+                            tma_load_3d(smem + i * C::QTILE + l * kLine, &maps.q, b, l * 64,
+                                        u.h * p.group, u.row0 + i * tpq);
                 }
                 __syncwarp();
-                return true;
+                if (NQ == 2) {
+                    for (int j = u.kb; ok && j < u.ke; ++j) {
+                        const int id2 = ids(j + 2);
+                        ok = load(&maps.k, j, 0, id) && load(&maps.v, j, 0, id);
+                        id = id_next;
+                        id_next = id2;
+                    }
+                } else {
+                    for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.k, u.kb, b, id);
+                    for (int j = u.kb; ok && j < u.ke; ++j) {
+                        const int id2 = ids(j + 2);
+                        if (j + 1 < u.ke)
+                            for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.k, j + 1, b, id_next);
+                        for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.v, j, b, id);
+                        id = id_next;
+                        id_next = id2;
+                    }
+                }
+            }
+            // every copy must land before the CTA exits
+            bool landed = true;
+            for (int i = max(0, boxes - N); i < boxes; ++i)
+                landed &= mbar_wait_bounded(bar(meta.full[i % N]), (i / N) & 1, kDrainWaitNs);
+            if (units > 0)
+                landed &= mbar_wait_bounded(bar(meta.q_full), (units - 1) & 1, kDrainWaitNs);
+            if (!landed) raise_flag(p.flags, kFlagTimeout);
+        } else if (warp == 9) {
+            // ================================================== MMA issue
+            constexpr uint32_t kIdS = mma_idesc(128, 128, !FP8, false);
+            constexpr uint32_t kIdO = mma_idesc(128, 128, !FP8, true);
+            const auto wait = [&](uint64_t &b, uint32_t parity) {
+                return warp_wait_soon(smem_u32(&b), parity, limit, p.flags);
             };
-            int id = ids(u.kb), id_next = ids(u.kb + 1);
-            if (!(ok = wait(meta.q_empty, (units & 1) ^ 1))) break;
-            ++units;
-            if (lane == 0) {
-                const uint32_t b = bar(meta.q_full);
-                int tiles = 0;
-                for (int i = 0; i < NQ; ++i) tiles += u.t[i].ntok > 0;
-                mbar_arrive_expect_tx(b, tiles * C::LINES * tpq * p.group * 128);
-                for (int i = 0; i < tiles; ++i)
-                    for (int l = 0; l < C::LINES; ++l)
-                        tma_load_3d(smem + i * C::QTILE + l * kLine, &maps.q, b, l * 64,
-                                    u.h * p.group, u.row0 + i * tpq);
-            }
-            __syncwarp();
-            if (NQ == 2) {
-                for (int j = u.kb; ok && j < u.ke; ++j) {
-                    const int id2 = ids(j + 2);
-                    ok = load(&maps.k, j, 0, id) && load(&maps.v, j, 0, id);
-                    id = id_next;
-                    id_next = id2;
-                }
-            } else {
-                for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.k, u.kb, b, id);
-                for (int j = u.kb; ok && j < u.ke; ++j) {
-                    const int id2 = ids(j + 2);
-                    if (j + 1 < u.ke)
-                        for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.k, j + 1, b, id_next);
-                    for (int b = 0; ok && b < C::BOXES; ++b) ok = load(&maps.v, j, b, id);
-                    id = id_next;
-                    id_next = id2;
-                }
-            }
-        }
-        // every copy must land before the CTA exits
-        bool landed = true;
-        for (int i = max(0, boxes - N); i < boxes; ++i)
-            landed &= mbar_wait_bounded(bar(meta.full[i % N]), (i / N) & 1, kDrainWaitNs);
-        if (units > 0)
-            landed &= mbar_wait_bounded(bar(meta.q_full), (units - 1) & 1, kDrainWaitNs);
-        if (!landed) raise_flag(p.flags, kFlagTimeout);
-    } else if (warp == 9) {
-        // ================================================== MMA issue
-        constexpr uint32_t kIdS = mma_idesc(128, 128, !FP8, false);
-        constexpr uint32_t kIdO = mma_idesc(128, 128, !FP8, true);
-        const auto wait = [&](uint64_t &b, uint32_t parity) {
-            return warp_wait_soon(smem_u32(&b), parity, limit, p.flags);
-        };
-        const uint32_t leader = elect_one();
-        int units = 0, steps = 0, slot = 0;
-        uint32_t phase = 0, fixed_phase = 0;
-        uint32_t p_count = 0;                        // parities, bit t of tile t
-        bool ok = true;
-        // S columns <- Q tile i . K box in slot s, elements 128 * half ...
-        const auto qk = [&](uint32_t d, int i, int s, int half) {
-            const uint64_t a = smem_desc(smem + i * C::QTILE + half * kBox, 16);
-            const uint64_t b = smem_desc(ring + s * kBox, 16);
-            if (elect_one()) {
+            const uint32_t leader = elect_one();
+            int units = 0, steps = 0, slot = 0;
+            uint32_t phase = 0, fixed_phase = 0;
+            uint32_t p_count = 0;                        // parities, bit t of tile t
+            bool ok = true;
+            // S columns <- Q tile i . K box in slot s, elements 128 * half ...
+            const auto qk = [&](uint32_t d, int i, int s, int half) {
+                const uint64_t a = smem_desc(smem + i * C::QTILE + half * kBox, 16);
+                const uint64_t b = smem_desc(ring + s * kBox, 16);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t off = ((kk >> 2) * kLine + (kk & 3) * 32) >> 4;
-                    mma_ss(tmem + d, a + off, b + off, kIdS, kk > 0 || half > 0);
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kLine + (kk & 3) * 32) >> 4;
+                        mma_ss(tmem + d, a + off, b + off, kIdS, kk > 0 || half > 0);
+                    }
                 }
-            }
-        };
-        // O columns (+)= P (in S columns c) . V box in slot s, one half of the keys
-        const auto pv = [&](uint32_t d, uint32_t c, int s, int half, bool acc) {
-            const uint64_t b = smem_desc(ring + s * kBox + half * 8192, kLine);
-            const uint32_t a = tmem + c + half * 32;
-            if (elect_one()) {
+            };
+            // O columns (+)= P (in S columns c) . V box in slot s, one half of the keys
+            const auto pv = [&](uint32_t d, uint32_t c, int s, int half, bool acc) {
+                const uint64_t b = smem_desc(ring + s * kBox + half * 8192, kLine);
+                const uint32_t a = tmem + c + half * 32;
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ts(tmem + d, a + kk * 8, b + kk * (2048 >> 4), kIdO, kk > 0 || acc);
-            }
-        };
-        uint64_t *ready = FP8 ? meta.fixed : meta.full;
-        // the ring's next box; its slot is returned, -1 after a timeout
-        const auto next_box = [&](bool fix) {
-            const int s = slot;
-            const bool fixed = FP8 || fix;
-            const uint32_t parity = !FP8 && fix ? (fixed_phase >> s) & 1 : phase;
-            if (!FP8 && fix) fixed_phase ^= 1u << s;
-            if (++slot == C::NS) {
-                slot = 0;
-                phase ^= 1;
-            }
-            return wait(fixed ? meta.fixed[s] : meta.full[s], parity) ? s : -1;
-        };
-        while (ok && next_piece()) {
-            const Piece k = meta.piece[piece % kPieces];
-            piece_read();
-            if (k.kb >= k.ke) continue;
-            if (!(ok = wait(FP8 ? meta.q_ready : meta.q_full, units & 1))) break;
-            ++units;
-            if (NQ == 2) {
-                int sk = next_box(false);
-                ok = sk >= 0;
-                if (!ok) break;
-                const int kb0 = k.t[0].kb, ke0 = k.t[0].ke;
-                const int kb1 = k.t[NQ - 1].kb, ke1 = k.t[NQ - 1].ke;
-#pragma unroll 1
-                for (int i = 0; i < NQ; ++i)
-                    if (i ? kb1 == k.kb && kb1 < ke1 : kb0 == k.kb && kb0 < ke0) {
-                        qk(i * 128, i, sk, 0);
-                        if (leader) mma_commit(bar(meta.s_ready[i]));
-                    }
-                if (leader) mma_commit(bar(meta.empty[sk]));
-                if (leader && k.kb + 1 == k.ke) mma_commit(bar(meta.q_empty));
-                // steps in which both tiles finish one key tile and start the
-                // next, and nothing else happens, run without conditions
-                const int steady_lo = max(max(kb0, kb1) + 1, k.part_lo);
-                const int steady_hi = min(min(ke0, ke1), k.part_hi) - 2;
-                for (int j = k.kb; ok && j < k.ke; ++j) {
-                    if (j >= steady_lo && j < steady_hi) {
-                        const int sv = slot, sn = slot + 1 == C::NS ? 0 : slot + 1;
-                        const uint32_t next_phase = phase ^ (slot + 1 == C::NS);
-                        ok = false;
-                        if (!wait(ready[sv], phase)) break;
-                        if (!wait(meta.p_ready[0][0], p_count & 1)) break;
-                        tcgen05_fence_after();
-                        pv(kOCol, 0, sv, 0, true);
-                        if (!wait(meta.p_ready[0][1], p_count & 1)) break;
-                        tcgen05_fence_after();
-                        pv(kOCol, 0, sv, 1, true);
-                        if (!wait(ready[sn], next_phase)) break;
-                        qk(0, 0, sn, 0);
-                        if (leader) mma_commit(bar(meta.s_ready[0]));
-                        if (!wait(meta.p_ready[1][0], p_count >> 1)) break;
-                        tcgen05_fence_after();
-                        pv(kOCol + 128, 128, sv, 0, true);
-                        if (!wait(meta.p_ready[1][1], p_count >> 1)) break;
-                        tcgen05_fence_after();
-                        pv(kOCol + 128, 128, sv, 1, true);
-                        if (leader) mma_commit(bar(meta.empty[sv]));
-                        qk(128, 1, sn, 0);
-                        if (leader) {
-                            mma_commit(bar(meta.s_ready[1]));
-                            mma_commit(bar(meta.empty[sn]));
-                        }
-                        p_count ^= 3;
-                        slot = sn + 1 == C::NS ? 0 : sn + 1;
-                        phase = next_phase ^ (sn + 1 == C::NS);
-                        ok = true;
-                        continue;
-                    }
-                    const bool more = j + 1 < k.ke;
-                    const int sv = next_box(is_partial(k, j));
-                    ok = sv >= 0;
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts(tmem + d, a + kk * 8, b + kk * (2048 >> 4), kIdO, kk > 0 || acc);
+                }
+            };
+            uint64_t *ready = FP8 ? meta.fixed : meta.full;
+            // the ring's next box; its slot is returned, -1 after a timeout
+            const auto next_box = [&](bool fix) {
+                const int s = slot;
+                const bool fixed = FP8 || fix;
+                const uint32_t parity = !FP8 && fix ? (fixed_phase >> s) & 1 : phase;
+                if (!FP8 && fix) fixed_phase ^= 1u << s;
+                if (++slot == C::NS) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                return wait(fixed ? meta.fixed[s] : meta.full[s], parity) ? s : -1;
+            };
+            while (ok && next_piece()) {
+                const Piece k = meta.piece[piece % kPieces];
+                piece_read();
+                if (k.kb >= k.ke) continue;
+                if (!(ok = wait(FP8 ? meta.q_ready : meta.q_full, units & 1))) break;
+                ++units;
+                if (NQ == 2) {
+                    int sk = next_box(false);
+                    ok = sk >= 0;
                     if (!ok) break;
+                    const int kb0 = k.t[0].kb, ke0 = k.t[0].ke;
+                    const int kb1 = k.t[NQ - 1].kb, ke1 = k.t[NQ - 1].ke;
 #pragma unroll 1
-                    for (int i = 0; i < NQ; ++i) {
-                        const int kb = i ? kb1 : kb0, ke = i ? ke1 : ke0;
-                        if (j >= kb && j < ke) {
-#pragma unroll 1
-                            for (int h = 0; h < 2; ++h) {
-                                ok = wait(meta.p_ready[i][h], (p_count >> i) & 1);
-                                if (!ok) break;
-                                tcgen05_fence_after();
-                                pv(kOCol + i * 128, i * 128, sv, h, h > 0 || j > kb);
-                            }
-                            if (!ok) break;
-                            p_count ^= 1u << i;
-                            if (j + 1 == ke && leader) mma_commit(bar(meta.o_done[i]));
-                        }
-                        if (i == NQ - 1 && leader) mma_commit(bar(meta.empty[sv]));
-                        if (i == 0 && more) {
-                            sk = next_box(false);
-                            ok = sk >= 0;
-                            if (!ok) break;
-                        }
-                        if (j + 1 >= kb && j + 1 < ke) {
+                    for (int i = 0; i < NQ; ++i)
+                        if (i ? kb1 == k.kb && kb1 < ke1 : kb0 == k.kb && kb0 < ke0) {
                             qk(i * 128, i, sk, 0);
                             if (leader) mma_commit(bar(meta.s_ready[i]));
                         }
-                    }
-                    if (!ok) break;
-                    if (leader && more) {
-                        mma_commit(bar(meta.empty[sk]));
-                        if (j + 2 == k.ke) mma_commit(bar(meta.q_empty));
-                    }
-                }
-            } else {
-                const auto qk_tile = [&](int step) {
-                    for (int b = 0; b < C::BOXES; ++b) {
-                        const int s = next_box(false);
-                        if (s < 0) return false;
-                        qk((step & 1) * 128, 0, s, b);
-                        if (leader) {
-                            mma_commit(bar(meta.empty[s]));
-                            if (b == C::BOXES - 1) mma_commit(bar(meta.s_ready[step & 1]));
-                        }
-                    }
-                    return true;
-                };
-                ok = qk_tile(steps);
-                if (ok && k.kb + 1 == k.ke && leader) mma_commit(bar(meta.q_empty));
-                for (int j = k.kb; ok && j < k.ke; ++j, ++steps) {
-                    if (j + 1 < k.ke) {
-                        if (!(ok = qk_tile(steps + 1))) break;
-                        if (j + 2 == k.ke && leader) mma_commit(bar(meta.q_empty));
-                    }
-#pragma unroll 1
-                    for (int b = 0; b < C::BOXES; ++b) {
-                        const int s = next_box(is_partial(k, j));
-                        ok = ok && s >= 0;
-#pragma unroll 1
-                        for (int h = 0; h < 2; ++h) {
-                            if (b == 0)
-                                ok = ok && wait(meta.p_ready[steps & 1][h], (steps >> 1) & 1);
-                            if (!ok) break;
+                    if (leader) mma_commit(bar(meta.empty[sk]));
+                    if (leader && k.kb + 1 == k.ke) mma_commit(bar(meta.q_empty));
+                    // steps in which both tiles finish one key tile and start the
+                    // next, and nothing else happens, run without conditions
+                    const int steady_lo = max(max(kb0, kb1) + 1, k.part_lo);
+                    const int steady_hi = min(min(ke0, ke1), k.part_hi) - 2;
+                    for (int j = k.kb; ok && j < k.ke; ++j) {
+                        if (j >= steady_lo && j < steady_hi) {
+                            const int sv = slot, sn = slot + 1 == C::NS ? 0 : slot + 1;
+                            const uint32_t next_phase = phase ^ (slot + 1 == C::NS);
+                            ok = false;
+                            if (!wait(ready[sv], phase)) break;
+                            if (!wait(meta.p_ready[0][0], p_count & 1)) break;
                             tcgen05_fence_after();
-                            pv(kOCol + b * 128, (steps & 1) * 128, s, h, h > 0 || j > k.kb);
+                            pv(kOCol, 0, sv, 0, true);
+                            if (!wait(meta.p_ready[0][1], p_count & 1)) break;
+                            tcgen05_fence_after();
+                            pv(kOCol, 0, sv, 1, true);
+                            if (!wait(ready[sn], next_phase)) break;
+                            qk(0, 0, sn, 0);
+                            if (leader) mma_commit(bar(meta.s_ready[0]));
+                            if (!wait(meta.p_ready[1][0], p_count >> 1)) break;
+                            tcgen05_fence_after();
+                            pv(kOCol + 128, 128, sv, 0, true);
+                            if (!wait(meta.p_ready[1][1], p_count >> 1)) break;
+                            tcgen05_fence_after();
+                            pv(kOCol + 128, 128, sv, 1, true);
+                            if (leader) mma_commit(bar(meta.empty[sv]));
+                            qk(128, 1, sn, 0);
+                            if (leader) {
+                                mma_commit(bar(meta.s_ready[1]));
+                                mma_commit(bar(meta.empty[sn]));
+                            }
+                            p_count ^= 3;
+                            slot = sn + 1 == C::NS ? 0 : sn + 1;
+                            phase = next_phase ^ (sn + 1 == C::NS);
+                            ok = true;
+                            continue;
+                        }
+                        const bool more = j + 1 < k.ke;
+                        const int sv = next_box(is_partial(k, j));
+                        ok = sv >= 0;
+                        if (!ok) break;
+#pragma unroll 1
+                        for (int i = 0; i < NQ; ++i) {
+                            const int kb = i ? kb1 : kb0, ke = i ? ke1 : ke0;
+                            if (j >= kb && j < ke) {
+#pragma unroll 1
+                                for (int h = 0; h < 2; ++h) {
+                                    ok = wait(meta.p_ready[i][h], (p_count >> i) & 1);
+                                    if (!ok) break;
+                                    tcgen05_fence_after();
+                                    pv(kOCol + i * 128, i * 128, sv, h, h > 0 || j > kb);
+                                }
+                                if (!ok) break;
+                                p_count ^= 1u << i;
+                                if (j + 1 == ke && leader) mma_commit(bar(meta.o_done[i]));
+                            }
+                            if (i == NQ - 1 && leader) mma_commit(bar(meta.empty[sv]));
+                            if (i == 0 && more) {
+                                sk = next_box(false);
+                                ok = sk >= 0;
+                                if (!ok) break;
+                            }
+                            if (j + 1 >= kb && j + 1 < ke) {
+                                qk(i * 128, i, sk, 0);
+                                if (leader) mma_commit(bar(meta.s_ready[i]));
+                            }
                         }
                         if (!ok) break;
-                        if (leader) mma_commit(bar(meta.empty[s]));
-                    }
-                    if (!ok) break;
-                    if (leader) mma_commit(bar(meta.pv_done));
-                    if (j + 1 == k.ke && leader) mma_commit(bar(meta.o_done[0]));
-                }
-            }
-        }
-        // the tensor cores must be done with shared and tensor memory
-        if (leader) mma_commit(bar(meta.drain));
-        if (!mbar_wait_bounded(bar(meta.drain), 0, kDrainWaitNs)) raise_flag(p.flags, kFlagTimeout);
-        __syncwarp();
-    } else if (warp >= C::V_WARP0) {
-        // ================================================== V warps
-        const int tid = threadIdx.x - C::V_WARP0 * 32;
-        int box = 0, units = 0;
-        bool ok = true;
-        while (ok && next_piece()) {
-            const Piece k = meta.piece[piece % kPieces];
-            piece_read();
-            if (k.kb >= k.ke) continue;
-            if (FP8) {
-                if (!(ok = wait(meta.q_full, units & 1))) break;
-#pragma unroll 1
-                for (int r = tid >> 3; r < (k.t[NQ - 1].ntok > 0 ? NQ : 1) * 128; r += 4 * C::V_WARPS) {
-                    const float back = convert_q_row(smem + (r >> 7) * C::QTILE, r & 127, tid & 7);
-                    if ((tid & 7) == 0) row_mult[(units & 1) * 256 + r] = back;
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(meta.q_ready));
-            }
-            ++units;
-            // one box: j its key tile, v whether it is of V
-            const auto take = [&](int j, bool v) {
-                const int s = box % C::NS;
-                const bool part = v && is_partial(k, j);
-                const int j0 = j * kKeys;
-                const int lo = part ? k.lo - j0 : 0, hi = part ? k.hi - j0 : kKeys;
-                bool bad = false;
-                if (!wait(meta.full[s], (box / C::NS) & 1)) return false;
-                if (FP8 || part) {
-                    if (FP8)
-                        bad = convert_box<C::V_WARPS>(ring + s * kBox, part, lo, hi, tid);
-                    else
-                        bad = clean_box<C::V_WARPS>(ring + s * kBox, lo, hi, k.all_lo - j0,
-                                                    k.all_hi - j0, tid);
-                    fence_proxy_async();
-                    if (bad) meta.redo[units % kRedoSlots] = units;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(meta.fixed[s]));
-                }
-                if (!FP8) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(meta.empty[s]));
-                }
-                ++box;
-                return true;
-            };
-            if (NQ == 2) {
-                for (int j = k.kb; ok && j < k.ke; ++j) ok = take(j, false) && take(j, true);
-            } else {
-                for (int b = 0; ok && b < C::BOXES; ++b) ok = take(k.kb, false);
-                for (int j = k.kb; ok && j < k.ke; ++j) {
-                    if (j + 1 < k.ke)
-                        for (int b = 0; ok && b < C::BOXES; ++b) ok = take(j + 1, false);
-                    for (int b = 0; ok && b < C::BOXES; ++b) ok = take(j, true);
-                }
-            }
-        }
-    }
-    } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX_REGS));
-    if (NQ == 2 || warp < 4) {
-        // ================================================== softmax
-        const int t = NQ == 2 ? warp >> 2 : 0;
-        const int r = threadIdx.x & 127;
-        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // TMEM lane 32 * (warp & 3)
-        const int g = p.group;
-        const int tok = r / g, hd = r - tok * g;
-        constexpr float kLog2e = 1.4426950408889634f;
-        int units = 0, steps = 0, done = 0;
-        bool ok = true;
-        // the piece stays in shared memory until its output is out
-        for (; ok && next_piece(); piece_read()) {
-            const Piece &u = meta.piece[piece % kPieces];
-            const TileKeys tk = u.t[t];
-            if (u.kb < u.ke) ++units;
-            if (tk.ntok <= 0) continue;
-            const bool valid = tok < tk.ntok;
-            const int hi = tk.p0 + tok + 1;
-            float m = -INFINITY, l = 0.f;
-            bool redo = false;
-            const bool any = tk.kb < tk.ke;
-            if (any) {
-                float mult = 0.f;
-                float2 l2 = make_float2(0.f, 0.f);
-                for (int j = tk.kb; j < tk.ke; ++j, ++steps) {
-                    const int sb = NQ == 2 ? t : steps & 1;
-                    if (!(ok = wait(meta.s_ready[sb], (NQ == 2 ? steps : steps >> 1) & 1))) break;
-                    tcgen05_fence_after();
-                    const uint32_t scol = tmem + lanes + sb * 128;
-                    if (j == tk.kb) {
-                        mult = p.scale * kLog2e;
-                        if (FP8) mult *= __ldg(p.k_scale + u.h) * row_mult[((units - 1) & 1) * 256 + t * 128 + r];
-                        // a scale of zero: every visible key weighs the same,
-                        // and masked scores (-inf) must still vanish
-                        if (mult == 0.f) mult = 0x1p-149f;
-                    }
-                    const bool masked = j < tk.mlo || j >= tk.mhi;
-                    if (__any_sync(0xffffffffu, masked || mult < 0.f)) {
-                        // scores are changed where they lie: hidden ones to
-                        // -inf, and all of them negated for a negative scale;
-                        // columns [b, a) are the row's
-                        const int a = masked ? hi - j * kKeys : kKeys;
-                        const int b = masked && p.window > 0 ? hi - p.window - j * kKeys : 0;
-#pragma unroll 1
-                        for (int c = 0; c < 128; c += 32) {
-                            if (!__any_sync(0xffffffffu, mult < 0.f || a < c + 32 || b > c)) continue;
-                            float s[32];
-                            if (!__any_sync(0xffffffffu, valid && a > c)) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) s[i] = -INFINITY;
-                            } else {
-                                tmem_ld32(scol + c, s);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) {
-                                    asm volatile("" : "+f"(s[i]));
-                                    s[i] = mult < 0.f ? -s[i] : s[i];
-                                    s[i] = c + i < a && c + i >= b ? s[i] : -INFINITY;
-                                }
-                            }
-                            tmem_st32(scol + c, s);
+                        if (leader && more) {
+                            mma_commit(bar(meta.empty[sk]));
+                            if (j + 2 == k.ke) mma_commit(bar(meta.q_empty));
                         }
-                        tmem_wait_st();
                     }
-                    // row maximum
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                } else {
+                    const auto qk_tile = [&](int step) {
+                        for (int b = 0; b < C::BOXES; ++b) {
+                            const int s = next_box(false);
+                            if (s < 0) return false;
+                            qk((step & 1) * 128, 0, s, b);
+                            if (leader) {
+                                mma_commit(bar(meta.empty[s]));
+                                if (b == C::BOXES - 1) mma_commit(bar(meta.s_ready[step & 1]));
+                            }
+                        }
+                        return true;
+                    };
+                    ok = qk_tile(steps);
+                    if (ok && k.kb + 1 == k.ke && leader) mma_commit(bar(meta.q_empty));
+                    for (int j = k.kb; ok && j < k.ke; ++j, ++steps) {
+                        if (j + 1 < k.ke) {
+                            if (!(ok = qk_tile(steps + 1))) break;
+                            if (j + 2 == k.ke && leader) mma_commit(bar(meta.q_empty));
+                        }
 #pragma unroll 1
-                    for (int c0 = 0; c0 < 128; c0 += 64) {
-                        float s[64];
-                        tmem_ld32(scol + c0, s);
-                        tmem_ld32(scol + c0 + 32, s + 32);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(s[c]));
-#pragma unroll
-                        for (int c = 0; c < 64; c += 8)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                m4[i] = max3_nan(m4[i], s[c + i], s[c + 4 + i]);
-                    }
-                    const float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
-                    const float am = fabsf(mult);
-                    const float top = valid ? mx * am : -INFINITY;
-                    // also for NaN, which poisons the row's sum, and +inf
-                    const bool move = !(top <= m + 8.f);
-                    if (__any_sync(0xffffffffu, move)) {
-                        const float m_new = move ? top : m;
-                        float alpha = move ? ex2(m - m_new) : 1.f;
-                        m = m_new;
-                        if (!(top < INFINITY)) alpha = l2.x = NAN;
-                        l2 = mul2(l2, make_float2(alpha, alpha));
-                        if (j > tk.kb) {
-                            if (NQ == 1) {
-                                if (!(ok = wait(meta.pv_done, (steps - 1) & 1))) break;
+                        for (int b = 0; b < C::BOXES; ++b) {
+                            const int s = next_box(is_partial(k, j));
+                            ok = ok && s >= 0;
+#pragma unroll 1
+                            for (int h = 0; h < 2; ++h) {
+                                if (b == 0)
+                                    ok = ok && wait(meta.p_ready[steps & 1][h], (steps >> 1) & 1);
+                                if (!ok) break;
                                 tcgen05_fence_after();
+                                pv(kOCol + b * 128, (steps & 1) * 128, s, h, h > 0 || j > k.kb);
                             }
-                            const uint32_t ocol = tmem + lanes + kOCol + t * 128;
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t o[16];
-                                tmem_ld16(ocol + c, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    asm volatile("" : "+r"(o[i]));
-                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                                }
-                                tmem_st16(ocol + c, o);
-                            }
+                            if (!ok) break;
+                            if (leader) mma_commit(bar(meta.empty[s]));
                         }
+                        if (!ok) break;
+                        if (leader) mma_commit(bar(meta.pv_done));
+                        if (j + 1 == k.ke && leader) mma_commit(bar(meta.o_done[0]));
                     }
-                    const float mu = m == -INFINITY ? 0.f : -m;
-                    const float2 k2 = make_float2(am, am), m2 = make_float2(mu, mu);
-                    // The scores are read a second time, in a short loop: all
-                    // warps of an SM run from one instruction cache, and with
-                    // the scores held in registers and the step unrolled it
-                    // took 3% longer; with every fourth pair of exponentials
-                    // as a polynomial on the FMA pipes 7% longer.
+                }
+            }
+            // the tensor cores must be done with shared and tensor memory
+            if (leader) mma_commit(bar(meta.drain));
+            if (!mbar_wait_bounded(bar(meta.drain), 0, kDrainWaitNs)) raise_flag(p.flags, kFlagTimeout);
+            __syncwarp();
+        } else if (warp >= C::V_WARP0) {
+            // ================================================== V warps
+            const int tid = threadIdx.x - C::V_WARP0 * 32;
+            int box = 0, units = 0;
+            bool ok = true;
+            while (ok && next_piece()) {
+                const Piece k = meta.piece[piece % kPieces];
+                piece_read();
+                if (k.kb >= k.ke) continue;
+                if (FP8) {
+                    if (!(ok = wait(meta.q_full, units & 1))) break;
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
+                    for (int r = tid >> 3; r < (k.t[NQ - 1].ntok > 0 ? NQ : 1) * 128; r += 4 * C::V_WARPS) {
+                        const float back = convert_q_row(smem + (r >> 7) * C::QTILE, r & 127, tid & 7);
+                        if ((tid & 7) == 0) row_mult[(units & 1) * 256 + r] = back;
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(meta.q_ready));
+                }
+                ++units;
+                // one box: j its key tile, v whether it is of V
+                const auto take = [&](int j, bool v) {
+                    const int s = box % C::NS;
+                    const bool part = v && is_partial(k, j);
+                    const int j0 = j * kKeys;
+                    const int lo = part ? k.lo - j0 : 0, hi = part ? k.hi - j0 : kKeys;
+                    bool bad = false;
+                    if (!wait(meta.full[s], (box / C::NS) & 1)) return false;
+                    if (FP8 || part) {
+                        if (FP8)
+                            bad = convert_box<C::V_WARPS>(ring + s * kBox, part, lo, hi, tid);
+                        else
+                            bad = clean_box<C::V_WARPS>(ring + s * kBox, lo, hi, k.all_lo - j0,
+                                                        k.all_hi - j0, tid);
+                        fence_proxy_async();
+                        if (bad) meta.redo[units % kRedoSlots] = units;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(meta.fixed[s]));
+                    }
+                    if (!FP8) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(meta.empty[s]));
+                    }
+                    ++box;
+                    return true;
+                };
+                if (NQ == 2) {
+                    for (int j = k.kb; ok && j < k.ke; ++j) ok = take(j, false) && take(j, true);
+                } else {
+                    for (int b = 0; ok && b < C::BOXES; ++b) ok = take(k.kb, false);
+                    for (int j = k.kb; ok && j < k.ke; ++j) {
+                        if (j + 1 < k.ke)
+                            for (int b = 0; ok && b < C::BOXES; ++b) ok = take(j + 1, false);
+                        for (int b = 0; ok && b < C::BOXES; ++b) ok = take(j, true);
+                    }
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX_REGS));
+        if (NQ == 2 || warp < 4) {
+            // ================================================== softmax
+            const int t = NQ == 2 ? warp >> 2 : 0;
+            const int r = threadIdx.x & 127;
+            const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // TMEM lane 32 * (warp & 3)
+            const int g = p.group;
+            const int tok = r / g, hd = r - tok * g;
+            constexpr float kLog2e = 1.4426950408889634f;
+            int units = 0, steps = 0, done = 0;
+            bool ok = true;
+            // the piece stays in shared memory until its output is out
+            for (; ok && next_piece(); piece_read()) {
+                const Piece &u = meta.piece[piece % kPieces];
+                const TileKeys tk = u.t[t];
+                if (u.kb < u.ke) ++units;
+                if (tk.ntok <= 0) continue;
+                const bool valid = tok < tk.ntok;
+                const int hi = tk.p0 + tok + 1;
+                float m = -INFINITY, l = 0.f;
+                bool redo = false;
+                const bool any = tk.kb < tk.ke;
+                if (any) {
+                    float mult = 0.f;
+                    float2 l2 = make_float2(0.f, 0.f);
+                    for (int j = tk.kb; j < tk.ke; ++j, ++steps) {
+                        const int sb = NQ == 2 ? t : steps & 1;
+                        if (!(ok = wait(meta.s_ready[sb], (NQ == 2 ? steps : steps >> 1) & 1))) break;
+                        tcgen05_fence_after();
+                        const uint32_t scol = tmem + lanes + sb * 128;
+                        if (j == tk.kb) {
+                            mult = p.scale * kLog2e;
+                            if (FP8) mult *= __ldg(p.k_scale + u.h) * row_mult[((units - 1) & 1) * 256 + t * 128 + r];
+                            // a scale of zero: every visible key weighs the same,
+                            // and masked scores (-inf) must still vanish
+                            if (mult == 0.f) mult = 0x1p-149f;
+                        }
+                        const bool masked = j < tk.mlo || j >= tk.mhi;
+                        if (__any_sync(0xffffffffu, masked || mult < 0.f)) {
+                            // scores are changed where they lie: hidden ones to
+                            // -inf, and all of them negated for a negative scale;
+                            // columns [b, a) are the row's
+                            const int a = masked ? hi - j * kKeys : kKeys;
+                            const int b = masked && p.window > 0 ? hi - p.window - j * kKeys : 0;
+#pragma unroll 1
+                            for (int c = 0; c < 128; c += 32) {
+                                if (!__any_sync(0xffffffffu, mult < 0.f || a < c + 32 || b > c)) continue;
+                                float s[32];
+                                if (!__any_sync(0xffffffffu, valid && a > c)) {
 #pragma unroll
-                        for (int c = 2 * h; c < 2 * h + 2; ++c) {
-                            float s[32];
-                            uint32_t w[16];
-                            tmem_ld32(scol + c * 32, s);
+                                    for (int i = 0; i < 32; ++i) s[i] = -INFINITY;
+                                } else {
+                                    tmem_ld32(scol + c, s);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) {
+                                        asm volatile("" : "+f"(s[i]));
+                                        s[i] = mult < 0.f ? -s[i] : s[i];
+                                        s[i] = c + i < a && c + i >= b ? s[i] : -INFINITY;
+                                    }
+                                }
+                                tmem_st32(scol + c, s);
+                            }
+                            tmem_wait_st();
+                        }
+                        // row maximum
+                        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                        for (int c0 = 0; c0 < 128; c0 += 64) {
+                            float s[64];
+                            tmem_ld32(scol + c0, s);
+                            tmem_ld32(scol + c0 + 32, s + 32);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(s[i]));
+                            for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(s[c]));
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                float2 x = fma2(make_float2(s[i], s[i + 1]), k2, m2);
-                                x.x = ex2(x.x);
-                                x.y = ex2(x.y);
-                                l2 = add2(l2, x);
-                                w[i / 2] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
-                            }
-                            tmem_st16(scol + c * 16, w);
+                            for (int c = 0; c < 64; c += 8)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    m4[i] = max3_nan(m4[i], s[c + i], s[c + 4 + i]);
                         }
-                        tmem_wait_st();
-                        tcgen05_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(meta.p_ready[sb][h]));
-                    }
-                }
-                if (!ok) break;
-                l = l2.x + l2.y;
-                if (!(ok = wait(meta.o_done[t], done & 1))) break;
-                ++done;
-                tcgen05_fence_after();
-                redo = reinterpret_cast<volatile uint32_t *>(meta.redo)[units % kRedoSlots] ==
-                       static_cast<uint32_t>(units);
-            }
-            const float vs = FP8 ? __ldg(p.v_scale + u.h) : 1.f;
-            if (redo) {
-                KvRows kv;
-                kv.flags = p.flags;
-                kv.head = u.h; kv.hkv = p.num_kv_heads; kv.bs = p.block_size;
-                kv.num_blocks = p.num_blocks;
-                kv.row_bytes = FP8 ? D : 2 * D;
-                kv.table = p.block_table ? p.block_table + static_cast<int64_t>(u.seq) * p.max_blocks_per_seq
-                                         : nullptr;
-                kv.k_stride = p.k_stride * 2;
-                kv.v_stride = p.v_stride * 2;
-                const int64_t off = p.block_table ? 0 : static_cast<int64_t>(u.h) * D * 2;
-                kv.k = static_cast<const uint8_t *>(p.k) + off + (p.block_table ? 0 : u.kv0 * kv.k_stride);
-                kv.v = static_cast<const uint8_t *>(p.v) + off + (p.block_table ? 0 : u.kv0 * kv.v_stride);
-                const float sl2 = p.scale * kLog2e * (FP8 ? __ldg(p.k_scale + u.h) : 1.f);
-                for (int rr = 0; rr < 32; ++rr) {
-                    const int ro = __shfl_sync(0xffffffffu, r, rr);
-                    const int tk_i = ro / g, hd_i = ro - tk_i * g;
-                    if (tk_i >= tk.ntok) continue;
-                    const int h1 = tk.p0 + tk_i + 1;
-                    const int a = max(p.window > 0 ? max(0, h1 - p.window) : 0, tk.kb * kKeys);
-                    const int b = min(h1, tk.ke * kKeys);
-                    const int64_t tr = u.row0 + t * tpq + tk_i;
-                    const int q1 = u.h * g + hd_i;
-                    float acc[D / 32], mm, ll;
-                    attend_row<D, FP8>(p.q + tr * p.q_stride + q1 * D, kv, a, b, sl2, acc, mm, ll);
-                    const float inv = ll == 0.f ? 0.f : vs / ll;
-                    const int64_t orow = tr * p.num_q_heads + q1;
-                    if (u.slot >= 0) {
-                        const int64_t pr = (static_cast<int64_t>(u.slot) * NQ + t) * 128 + ro;
-                        for (int i = 0; i < D / 32; ++i)
-                            p.o_part[pr * D + lane * (D / 32) + i] = acc[i] * inv;
-                        if (lane == 0)
-                            p.lse_part[pr] = ll == 0.f ? -INFINITY : mm * 0.6931471805599453f + logf(ll);
-                    } else {
-                        uint32_t *o = reinterpret_cast<uint32_t *>(p.out + orow * D) + lane * (D / 64);
-                        for (int i = 0; i < D / 64; ++i)
-                            o[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-                        if (p.lse_out && lane == 0)
-                            p.lse_out[orow] = ll == 0.f ? -INFINITY : mm * 0.6931471805599453f + logf(ll);
-                    }
-                }
-                continue;
-            }
-            const bool dead = l == 0.f;
-            const float inv = dead ? 0.f : vs / l;
-            const float lse = dead ? -INFINITY : m * 0.6931471805599453f + logf(l);
-            // A thread writes its row, 32 bytes (a sector) at a time.
-            const bool part = u.slot >= 0;
-            const int64_t orow = part ? (static_cast<int64_t>(u.slot) * NQ + t) * 128 + r
-                                      : static_cast<int64_t>(u.row0 + t * tpq + tok) * p.num_q_heads +
-                                            u.h * g + hd;
+                        const float mx = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]);
+                        const float am = fabsf(mult);
+                        const float top = valid ? mx * am : -INFINITY;
+                        // also for NaN, which poisons the row's sum, and +inf
+                        const bool move = !(top <= m + 8.f);
+                        if (__any_sync(0xffffffffu, move)) {
+                            const float m_new = move ? top : m;
+                            float alpha = move ? ex2(m - m_new) : 1.f;
+                            m = m_new;
+                            if (!(top < INFINITY)) alpha = l2.x = NAN;
+                            l2 = mul2(l2, make_float2(alpha, alpha));
+                            if (j > tk.kb) {
+                                if (NQ == 1) {
+                                    if (!(ok = wait(meta.pv_done, (steps - 1) & 1))) break;
+                                    tcgen05_fence_after();
+                                }
+                                const uint32_t ocol = tmem + lanes + kOCol + t * 128;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                if (any) {
-                    tmem_ld32(tmem + lanes + kOCol + t * 128 + c, o);
-                    tmem_wait_ld();
+                                for (int c = 0; c < D; c += 16) {
+                                    uint32_t o[16];
+                                    tmem_ld16(ocol + c, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) {
+                                        asm volatile("" : "+r"(o[i]));
+                                        o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                                    }
+                                    tmem_st16(ocol + c, o);
+                                }
+                            }
+                        }
+                        const float mu = m == -INFINITY ? 0.f : -m;
+                        const float2 k2 = make_float2(am, am), m2 = make_float2(mu, mu);
+                        // The scores are read a second time, in a short loop: with
+                        // three quarters of them held in registers and the step
+                        // unrolled a prompt of 8192 tokens took 951 us instead of
+                        // 1007, a mixed step 114 instead of 112 and windowed wide
+                        // heads 191 instead of 185.  Every fourth pair of
+                        // exponentials as a polynomial on the FMA pipes relieves
+                        // ex2 (8 cycles a warp instruction) but took 121 us of the
+                        // mixed step, and no less of the prompt.
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                                float s[32];
+                                uint32_t w[16];
+                                tmem_ld32(scol + c * 32, s);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(s[i]));
+#pragma unroll
+                                for (int i = 0; i < 32; i += 2) {
+                                    float2 x = fma2(make_float2(s[i], s[i + 1]), k2, m2);
+                                    x.x = ex2(x.x);
+                                    x.y = ex2(x.y);
+                                    l2 = add2(l2, x);
+                                    w[i / 2] = FP8 ? pack_f16x2(x.x, x.y) : pack_bf16x2(x.x, x.y);
+                                }
+                                tmem_st16(scol + c * 16, w);
+                            }
+                            tmem_wait_st();
+                            tcgen05_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(meta.p_ready[sb][h]));
+                        }
+                    }
+                    if (!ok) break;
+                    l = l2.x + l2.y;
+                    if (!(ok = wait(meta.o_done[t], done & 1))) break;
+                    ++done;
+                    tcgen05_fence_after();
+                    redo = reinterpret_cast<volatile uint32_t *>(meta.redo)[units % kRedoSlots] ==
+                           static_cast<uint32_t>(units);
                 }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(o[i]));
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = dead ? 0.f : o[i] * inv;
-                if (!valid) continue;
-                if (part) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 8)
-                        store32(p.o_part + orow * D + c + i, o + i);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 16) {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(o[i + 2 * k], o[i + 2 * k + 1]);
-                        uint16_t *dst = p.out + orow * D + c + i;
-                        if (p.out32) {
-                            store32(dst, w);
+                const float vs = FP8 ? __ldg(p.v_scale + u.h) : 1.f;
+                if (redo) {
+                    KvRows kv;
+                    kv.flags = p.flags;
+                    kv.head = u.h; kv.hkv = p.num_kv_heads; kv.bs = p.block_size;
+                    kv.num_blocks = p.num_blocks;
+                    kv.row_bytes = FP8 ? D : 2 * D;
+                    kv.table = p.block_table ? p.block_table + static_cast<int64_t>(u.seq) * p.max_blocks_per_seq
+                                             : nullptr;
+                    kv.k_stride = p.k_stride * 2;
+                    kv.v_stride = p.v_stride * 2;
+                    const int64_t off = p.block_table ? 0 : static_cast<int64_t>(u.h) * D * 2;
+                    kv.k = static_cast<const uint8_t *>(p.k) + off + (p.block_table ? 0 : u.kv0 * kv.k_stride);
+                    kv.v = static_cast<const uint8_t *>(p.v) + off + (p.block_table ? 0 : u.kv0 * kv.v_stride);
+                    const float sl2 = p.scale * kLog2e * (FP8 ? __ldg(p.k_scale + u.h) : 1.f);
+                    for (int rr = 0; rr < 32; ++rr) {
+                        const int ro = __shfl_sync(0xffffffffu, r, rr);
+                        const int tk_i = ro / g, hd_i = ro - tk_i * g;
+                        if (tk_i >= tk.ntok) continue;
+                        const int h1 = tk.p0 + tk_i + 1;
+                        const int a = max(p.window > 0 ? max(0, h1 - p.window) : 0, tk.kb * kKeys);
+                        const int b = min(h1, tk.ke * kKeys);
+                        const int64_t tr = u.row0 + t * tpq + tk_i;
+                        const int q1 = u.h * g + hd_i;
+                        float acc[D / 32], mm, ll;
+                        attend_row<D, FP8>(p.q + tr * p.q_stride + q1 * D, kv, a, b, sl2, acc, mm, ll);
+                        const float inv = ll == 0.f ? 0.f : vs / ll;
+                        const int64_t orow = tr * p.num_q_heads + q1;
+                        if (u.slot >= 0) {
+                            const int64_t pr = (static_cast<int64_t>(u.slot) * NQ + t) * 128 + ro;
+                            for (int i = 0; i < D / 32; ++i)
+                                p.o_part[pr * D + lane * (D / 32) + i] = acc[i] * inv;
+                            if (lane == 0)
+                                p.lse_part[pr] = ll == 0.f ? -INFINITY : mm * 0.6931471805599453f + logf(ll);
                         } else {
-                            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-                            *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                            uint32_t *o = reinterpret_cast<uint32_t *>(p.out + orow * D) + lane * (D / 64);
+                            for (int i = 0; i < D / 64; ++i)
+                                o[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+                            if (p.lse_out && lane == 0)
+                                p.lse_out[orow] = ll == 0.f ? -INFINITY : mm * 0.6931471805599453f + logf(ll);
+                        }
+                    }
+                    continue;
+                }
+                const bool dead = l == 0.f;
+                const float inv = dead ? 0.f : vs / l;
+                const float lse = dead ? -INFINITY : m * 0.6931471805599453f + logf(l);
+                // A thread writes its row, 32 bytes (a sector) at a time.
+                const bool part = u.slot >= 0;
+                const int64_t orow = part ? (static_cast<int64_t>(u.slot) * NQ + t) * 128 + r
+                                          : static_cast<int64_t>(u.row0 + t * tpq + tok) * p.num_q_heads +
+                                                u.h * g + hd;
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    if (any) {
+                        tmem_ld32(tmem + lanes + kOCol + t * 128 + c, o);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(o[i]));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = dead ? 0.f : o[i] * inv;
+                    if (!valid) continue;
+                    if (part) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            store32(p.o_part + orow * D + c + i, o + i);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 16) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(o[i + 2 * k], o[i + 2 * k + 1]);
+                            uint16_t *dst = p.out + orow * D + c + i;
+                            if (p.out32) {
+                                store32(dst, w);
+                            } else {
+                                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                                *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                            }
                         }
                     }
                 }
-            }
-            // the next piece's first P, by the same warps, tells that O was read
-            tcgen05_fence_before();
-            if (valid) {
-                if (part) p.lse_part[orow] = lse;
-                else if (p.lse_out) p.lse_out[orow] = lse;
+                // the next piece's first P, by the same warps, tells that O was read
+                tcgen05_fence_before();
+                if (valid) {
+                    if (part) p.lse_part[orow] = lse;
+                    else if (p.lse_out) p.lse_out[orow] = lse;
+                }
             }
         }
-    }
     }
     tcgen05_fence_before();
     __syncthreads();
