@@ -50,9 +50,9 @@
 // 1330) leaves both busy 0.55 - 0.6 of the time.  64 heads over 8, 8192 tokens:
 // 980 - 1040 us, 1.06 - 1.12 PFLOP/s at the power cap (992 W, 1.74 GHz), where
 // plain matrix products sustain 1.39.  Every instruction of the MMA warp
-// counts: descriptors built per product (18 instructions each), branches and
-// 64-bit compares before a wait and conditions in the loop cost 5400 cycles a
-// step, the straight form 3700.
+// counts: descriptors built per product (18 instructions each by the code's
+// size, 4 now), branches and 64-bit compares before a wait and conditions in
+// the loop cost 5400 cycles a step, the straight form 3700.
 //
 // Every wait is bounded (wait_ns): a role that gives up raises the timeout
 // flag and leaves; the producer and the MMA warp then wait for what they have

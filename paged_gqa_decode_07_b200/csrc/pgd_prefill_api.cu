@@ -42,8 +42,12 @@ pgd_status check_common(int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
     return PGD_OK;
 }
 
-// Units are cut from this many keys on (the host's bound on a sequence's).
-constexpr int64_t kCutKeys = 1024;
+// Units are cut from this many keys on (the host's bound on what a unit's rows
+// see).  Whole / cut, us, 32 heads over 8 of 128: one new token after 768 keys
+// 18.0 / 19.4, 1280: 25.7 / 22.1, 2048: 36.9 / 26.6; a prompt of 1024 26.6 /
+// 35.1, 1280: 45.4 / 42.4, 1792: 60.6 / 51.7; four prompts 42.5 / 57.1, 70.2 /
+// 68.9, 110.4 / 107.7; 8192 tokens with a window of 1024 163 / 180.
+constexpr int64_t kCutKeys = 1280;
 
 // Grid, and whether units are cut: one CTA per SM, one per unit where they
 // stay whole.  Cutting costs the merge kernel (about 4 us) and evens out

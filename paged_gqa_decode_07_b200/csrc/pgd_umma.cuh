@@ -89,9 +89,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r) {
 //   MN-major operand (rows = K, contiguous = N): a line is 64 elements of N,
 //     lines are `line` bytes apart; 8-row groups of K are 1024 bytes apart, so
 //     16 of K are 2048 bytes further.
-// A batch of MMAs adds (byte offset >> 4) to a base descriptor, which the
-// compiler then keeps in uniform registers: 4 instructions an MMA, where
-// descriptors built from addresses took 18.
+// A batch of MMAs adds (byte offset >> 4) to a base descriptor made once: by the
+// code's size 4 instructions an MMA, where descriptors built from addresses
+// took 18.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
     return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
            (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
