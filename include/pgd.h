@@ -310,7 +310,8 @@ pgd_status pgd_paged_decode_attention_ex(
  *                1 .. 16; head_dim in {128, 256}
  *   out          device bf16 [num_tokens][num_q_heads][head_dim], 16-byte
  *                aligned (rounded once, from fp32)
- *   lse_out      optional device fp32 [num_tokens][num_q_heads] (natural log)
+ *   lse_out      optional device fp32 [num_tokens][num_q_heads] (natural log);
+ *                neither overlaps an input
  *   workspace, workspace_bytes, num_ctas   the work (query rows times keys) is
  *                dealt in equal shares to num_ctas CTAs; 0 = automatic, 1 ..
  *                1024 forces a number.  The query rows whose keys a boundary

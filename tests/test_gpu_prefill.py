@@ -655,3 +655,49 @@ def test_a_scale_of_zero_weighs_large_scores_alike():
     out, lse = run_packed(q, k, v, cu_t, 4, 2, 128, 0.0)
     ref = prefill_ref.packed(q, k, v, cu, 0, 0.0)
     prefill_ref.assert_within(out, lse, ref, 140, 128, "bf16")
+
+
+@pytest.mark.parametrize("ctas", [0, 7])
+@pytest.mark.parametrize("dt", ["bf16", "e4m3"])
+def test_a_captured_call_follows_new_lengths(ctas, dt):
+    """A serving loop captures one step and replays it as sequences grow,
+    begin, end and change their share of the rows."""
+    hq, hkv, d, bs = 8, 2, 128, 16
+    full = [1700, 300, 1500, 40]
+    kc, vc, table, ks, vs = make_pages(full, hkv, d, bs, dt, 190)
+    T = 96
+    q = randn((T, hq, d), 191)
+    scale = 1 / math.sqrt(d)
+    cl = torch.tensor(full, dtype=torch.int32, device="cuda")
+    cu_t = torch.tensor([0, 40, 41, 90, 96], dtype=torch.int32, device="cuda")
+    out = torch.empty((T, hq, d), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((T, hq), device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pgd.paged_prefill_attention(q, kc, vc, table, cl, cu_t, hq, hkv, d, bs, scale, out,
+                                    lse_out=lse, k_scale=ks, v_scale=vs, max_context_len=1700,
+                                    num_ctas=ctas)
+    for ctx, cu in ((full, [0, 40, 41, 90, 96]), ([1, 300, 0, 7], [0, 1, 90, 90, 94]),
+                    ([1699, 0, 1281, 40], [0, 0, 0, 95, 96]), ([0, 0, 0, 0], [0, 0, 0, 0, 0])):
+        cl.copy_(torch.tensor(ctx, dtype=torch.int32))
+        cu_t.copy_(torch.tensor(cu, dtype=torch.int32))
+        out.fill_(SENTINEL)
+        lse.fill_(SENTINEL)
+        g.replay()
+        torch.cuda.synchronize()
+        # contexts shorter than the pages: what lies behind them has no influence
+        ref = prefill_ref.paged(q, fp8(kc), fp8(vc), table, ctx, cu, 0, scale, ks, vs)
+        a, b = cu[0], cu[-1]
+        if b > a:
+            prefill_ref.assert_within(out[a:b], lse[a:b], [r[a:b] for r in ref], max(ctx), d, dt,
+                                      f"{ctx} {cu}")
+        for x in (out, lse):
+            assert bool((x[b:] == SENTINEL).all())
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("n", [1279, 1280, 1281])
+def test_lengths_around_where_work_is_cut(n, d):
+    assert (pgd.prefill_workspace_bytes(1, n, n, 0, 4, 2, d) > 0) == (n >= 1280)
+    check_packed([n], 4, 2, d, seed=n)
+    check_paged([3, 0], [n, 0], 4, 2, d, 16, "bf16", seed=n)
