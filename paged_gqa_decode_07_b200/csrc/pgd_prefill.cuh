@@ -54,6 +54,9 @@
 // size, 4 now), branches and 64-bit compares before a wait and conditions in
 // the loop cost 5400 cycles a step, the straight form 3700.
 //
+// Tensor-memory loads and stores are warp-wide (.sync.aligned): between two of
+// them lanes differ only by predicates and selects, or meet at a __syncwarp.
+//
 // Every wait is bounded (wait_ns): a role that gives up raises the timeout
 // flag and leaves; the producer and the MMA warp then wait for what they have
 // in flight, all warps meet, and tensor memory is freed.
@@ -747,7 +750,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                             if (FP8) mult *= __ldg(p.k_scale + u.h) * row_mult[((units - 1) & 1) * 256 + t * 128 + r];
                             // a scale of zero: every visible key weighs the same,
                             // and masked scores (-inf) must still vanish
-                            if (mult == 0.f) mult = 0x1p-149f;
+                            mult = mult == 0.f ? 0x1p-149f : mult;
                         }
                         const bool masked = j < tk.mlo || j >= tk.mhi;
                         if (__any_sync(0xffffffffu, masked || mult < 0.f)) {
@@ -802,7 +805,8 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                             const float m_new = move ? top : m;
                             float alpha = move ? ex2(m - m_new) : 1.f;
                             m = m_new;
-                            if (!(top < INFINITY)) alpha = l2.x = NAN;
+                            alpha = top < INFINITY ? alpha : NAN;
+                            l2.x = top < INFINITY ? l2.x : NAN;
                             l2 = mul2(l2, make_float2(alpha, alpha));
                             if (j > tk.kb) {
                                 if (NQ == 1) {
@@ -857,7 +861,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                             tmem_wait_st();
                             tcgen05_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(bar(meta.p_ready[sb][h]));
+                            mbar_arrive_if(bar(meta.p_ready[sb][h]), lane == 0);
                         }
                     }
                     if (!ok) break;
@@ -931,12 +935,11 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                     for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(o[i]));
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = dead ? 0.f : o[i] * inv;
-                    if (!valid) continue;
-                    if (part) {
+                    if (valid && part) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 8)
                             store32(p.o_part + orow * D + c + i, o + i);
-                    } else {
+                    } else if (valid) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 16) {
                             uint32_t w[8];
@@ -951,6 +954,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                             }
                         }
                     }
+                    __syncwarp();                // lanes with and without a row meet again
                 }
                 // the next piece's first P, by the same warps, tells that O was read
                 tcgen05_fence_before();
@@ -961,6 +965,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             }
         }
     }
+    __syncwarp();
     tcgen05_fence_before();
     __syncthreads();
     if (warp == 9) {

@@ -45,6 +45,13 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
                  ::"r"(bar) : "memory");
 }
 
+// The same where `pred` holds, without a branch around it.
+__device__ __forceinline__ void mbar_arrive_if(uint32_t bar, bool pred) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 st;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+                 "@p mbarrier.arrive.shared::cta.b64 st, [%0];\n\t}"
+                 ::"r"(bar), "r"(static_cast<uint32_t>(pred)) : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("{\n\t.reg .b64 st;\n\t"
                  "mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}"
