@@ -176,6 +176,28 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new(shape, dtype, device, stream, shared: bool = True) -> torch.Tensor:
+    """A tensor that a call on `stream` writes, from that stream's pool.
+
+    The allocator hands a block out again in the order of its pool's stream: one
+    of the current stream's pool may still be in use there when work on another
+    stream begins.  `shared`: the caller gets the tensor and may read it on the
+    current stream, so the block also waits for that one when it is freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream
+    if not isinstance(s, torch.cuda.Stream):
+        # a handle of 0 is the default stream, which ExternalStream cannot name
+        handle = _stream(stream)
+        s = torch.cuda.ExternalStream(handle, device=device) if handle else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if shared:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _kv_dtype(cache: torch.Tensor) -> int:
     if cache.dtype == torch.bfloat16:
         return PGD_KV_BF16
@@ -281,7 +303,7 @@ def paged_decode_attention(q, k_cache, v_cache, block_table, context_lens, num_q
         _need(k_scale, "k_scale", (torch.float32,), 1)
         _need(v_scale, "v_scale", (torch.float32,), 1)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     _need(out, "out", (torch.bfloat16,), 3)
     if lse_out is not None:
         _need(lse_out, "lse_out", (torch.float32,), 2)
@@ -326,7 +348,7 @@ def paged_decode_attention_ex(q, k_cache, v_cache, block_table, context_lens, nu
         _need(k_scale, "k_scale", (torch.float32,), 1)
         _need(v_scale, "v_scale", (torch.float32,), 1)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     _need(out, "out", (torch.bfloat16,), 4)
     if lse_out is not None:
         _need(lse_out, "lse_out", (torch.float32,), 3)
@@ -367,9 +389,9 @@ def paged_decode_partial(q, k_cache, v_cache, block_table, context_lens, num_q_h
         _need(k_scale, "k_scale", (torch.float32,), 1)
         _need(v_scale, "v_scale", (torch.float32,), 1)
     if o_part is None:
-        o_part = torch.empty((B, num_q_heads, head_dim), dtype=torch.float32, device=q.device)
+        o_part = _new((B, num_q_heads, head_dim), torch.float32, q.device, stream)
     if lse_part is None:
-        lse_part = torch.empty((B, num_q_heads), dtype=torch.float32, device=q.device)
+        lse_part = _new((B, num_q_heads), torch.float32, q.device, stream)
     _need(o_part, "o_part", (torch.float32,), 3)
     _need(lse_part, "lse_part", (torch.float32,), 2)
     if o_part.shape != (B, num_q_heads, head_dim) or lse_part.shape != (B, num_q_heads):
@@ -471,7 +493,7 @@ def decode_step(q, k_new, v_new, k_cache, v_cache, block_table, context_lens, nu
         _need(k_scale, "k_scale", (torch.float32,), 1)
         _need(v_scale, "v_scale", (torch.float32,), 1)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     _need(out, "out", (torch.bfloat16,), 3)
     if lse_out is not None:
         _need(lse_out, "lse_out", (torch.float32,), 2)
@@ -514,7 +536,7 @@ def paged_decode_attention_noalloc(q, k_cache, v_cache, block_table, context_len
         _need(k_scale, "k_scale", (torch.float32,), 1)
         _need(v_scale, "v_scale", (torch.float32,), 1)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     _need(out, "out", (torch.bfloat16,), 3)
     if lse_out is not None:
         _need(lse_out, "lse_out", (torch.float32,), 2)
@@ -536,7 +558,7 @@ def merge_partials(o_part, lse_part, out=None, lse_out=None, *, stream=None, pre
     if lse_part.shape != (P, R):
         raise ValueError("merge_partials: inconsistent shapes")
     if out is None:
-        out = torch.empty((R, D), dtype=torch.bfloat16, device=o_part.device)
+        out = _new((R, D), torch.bfloat16, o_part.device, stream)
     _need(out, "out", (torch.bfloat16,), 2)
     if lse_out is not None:
         _need(lse_out, "lse_out", (torch.float32,), 1)
@@ -576,19 +598,14 @@ def _rows(t, name: str, heads: int, dim: int) -> int:
 
 
 def _prefill_workspace(workspace, need: int, device, stream):
-    """(workspace, bytes): the caller's, or one from torch's allocator on the
-    launching stream when the call can use one."""
+    """(workspace, bytes): the caller's, or one from the pool of the launching
+    stream when the call can use one."""
     if workspace is not None:
         _need(workspace, "workspace", None)
         return workspace, workspace.numel() * workspace.element_size()
     if need == 0:
         return None, 0
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    if isinstance(stream, torch.cuda.Stream):
-        ws.record_stream(stream)
-    elif stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(int(stream)))
-    return ws, need
+    return _new((need,), torch.uint8, device, stream, shared=False), need
 
 
 @functools.lru_cache(maxsize=256)
@@ -630,7 +647,7 @@ def prefill_attention(q, k, v, cu_seqlens, num_q_heads: int, num_kv_heads: int, 
     if k.size(0) != T or v.size(0) != T or B < 0:
         raise ValueError("prefill_attention: inconsistent shapes")
     if out is None:
-        out = torch.empty((T, num_q_heads, head_dim), dtype=torch.bfloat16, device=q.device)
+        out = _new((T, num_q_heads, head_dim), torch.bfloat16, q.device, stream)
     _need(out, "out", (torch.bfloat16,), 3)
     if lse_out is not None:
         _need(lse_out, "lse_out", (torch.float32,), 2)
@@ -683,7 +700,7 @@ def paged_prefill_attention(q, k_cache, v_cache, block_table, context_lens, cu_s
     else:
         k_scale = v_scale = None
     if out is None:
-        out = torch.empty((T, num_q_heads, head_dim), dtype=torch.bfloat16, device=q.device)
+        out = _new((T, num_q_heads, head_dim), torch.bfloat16, q.device, stream)
     _need(out, "out", (torch.bfloat16,), 3)
     if lse_out is not None:
         _need(lse_out, "lse_out", (torch.float32,), 2)
@@ -718,9 +735,9 @@ def kv_quant_scales(k_new, v_new, k_scale: Optional[torch.Tensor] = None,
     if accumulate and (k_scale is None or v_scale is None):
         raise ValueError("kv_quant_scales: accumulate needs k_scale and v_scale")
     if k_scale is None:
-        k_scale = torch.empty(hkv, dtype=torch.float32, device=k_new.device)
+        k_scale = _new((hkv,), torch.float32, k_new.device, stream)
     if v_scale is None:
-        v_scale = torch.empty(hkv, dtype=torch.float32, device=k_new.device)
+        v_scale = _new((hkv,), torch.float32, k_new.device, stream)
     _need(k_scale, "k_scale", (torch.float32,), 1)
     _need(v_scale, "v_scale", (torch.float32,), 1)
     if v_new.shape != k_new.shape or k_scale.shape != (hkv,) or v_scale.shape != (hkv,):
@@ -753,9 +770,9 @@ def kv_gather(k_cache, v_cache, slot_mapping, k_out: Optional[torch.Tensor] = No
     else:
         k_scale = v_scale = None
     if k_out is None:
-        k_out = torch.empty((n, hkv, d), dtype=torch.bfloat16, device=k_cache.device)
+        k_out = _new((n, hkv, d), torch.bfloat16, k_cache.device, stream)
     if v_out is None:
-        v_out = torch.empty((n, hkv, d), dtype=torch.bfloat16, device=k_cache.device)
+        v_out = _new((n, hkv, d), torch.bfloat16, k_cache.device, stream)
     _need(k_out, "k_out", (torch.bfloat16,), 3)
     _need(v_out, "v_out", (torch.bfloat16,), 3)
     if v_cache.shape != k_cache.shape or tuple(k_out.shape) != (n, hkv, d) or \
