@@ -47,11 +47,13 @@ struct Piece {
     TileKeys t[2];
 };
 
-// Where a CTA's share starts, and how long it is.
+// Where a CTA's share starts, and how long it is.  More CTAs than the axis is
+// long leave shares of no length: they have a start all the same, which the
+// merge needs to follow a unit's pieces from CTA to CTA.
 struct Share {
     long long at, len;               // offset into the sequence's units, length
     long long seq_start;             // axis position of the sequence
-    int seq;
+    int seq;                         // num_seqs: no work at all
     long long warp_sum[kMaxThreads / 32];
 };
 
@@ -155,7 +157,7 @@ __device__ void find_share(const PrefillParams &p, Share &share) {
                 continue;
             }
             const long long a = base + incl - mine;
-            if (x0 < x1 && mine > 0 && a <= x0 && x0 < a + mine) {
+            if (mine > 0 && a <= x0 && x0 < a + mine) {
                 share.at = x0 - a;
                 share.len = x1 - x0;
                 share.seq_start = a;
@@ -264,7 +266,7 @@ struct PieceWalk {
           unit_start(share.seq_start), seq(share.seq), h(0), unit(0), units(0), window_seq(-64) {
         int cut = 0;
         if (!p.parts) return;
-        if (len > 0) {
+        if (seq < p.num_seqs) {
             load_seq();
             const long long per_head = units_len(s, tpu, units, p.window, units);
             h = static_cast<int>(share.at / per_head);

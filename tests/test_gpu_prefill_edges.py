@@ -31,3 +31,28 @@ def test_every_count_of_rows_in_a_warp(d, dt, hq, hkv, ctas):
         check_packed(lens, hq, hkv, d, seed=300, num_ctas=ctas, tail=3)
     check_paged(lens, [n + 3 * i for i, n in enumerate(lens)], hq, hkv, d, 16, dt, seed=301,
                 num_ctas=ctas, tail=3)
+
+
+# --------------------------------------------------------------------------- #
+# More shares than the work is long                                           #
+# --------------------------------------------------------------------------- #
+def nan_workspace(seqs, tokens, keys, hq, hkv, d, ctas):
+    """A workspace in which a slot that nothing wrote shows."""
+    need = pgd.prefill_workspace_bytes(seqs, tokens, keys, 0, hq, hkv, d, ctas)
+    assert need % 4 == 0 and need > 0
+    return torch.full((need // 4,), float("nan"), device="cuda")
+
+
+@pytest.mark.parametrize("ctas", [600, 700, 1000, 1024])
+@pytest.mark.parametrize("d,dt", [(128, "bf16"), (256, "bf16"), (128, "e4m3")])
+def test_more_ctas_than_the_axis_is_long(d, dt, ctas):
+    """A unit is its keys and a constant long: some CTAs get nothing, and their
+    boundaries lie inside a unit that others cut."""
+    for ctx in (130, 200, 257, 384, 516, 600, 640, 700):
+        check_paged([1], [ctx], 4, 1, d, 16, dt, seed=310 + ctx, num_ctas=ctas,
+                    workspace=nan_workspace(1, 1, ctx, 4, 1, d, ctas))
+    check_paged([200, 0, 3], [200, 9, 20], 2, 1, d, 16, dt, seed=311, num_ctas=ctas,
+                workspace=nan_workspace(3, 203, 200, 2, 1, d, ctas))
+    if dt == "bf16":
+        check_packed([200], 1, 1, d, seed=312, num_ctas=ctas,
+                     workspace=nan_workspace(1, 200, 200, 1, 1, d, ctas))
