@@ -38,12 +38,15 @@
 // P enters the product as bf16 (f16 for FP8 caches, whose V is exact there);
 // l sums the unrounded weights.
 //
-// Masked keys.  A masked weight is zero, but zero times a V row that is not
+// Masked keys.  A masked weight is zero, but zero times a value that is not
 // finite is NaN, and rows of unowned slots may hold anything.  On key tiles
 // that some row does not fully see, the V warps zero the rows no query of the
-// unit sees before the product reads them, and look for non-finite values in
-// the rest; where there is one, the unit's rows are computed again one warp
-// per row from the definition (attend_row), which touches visible keys only.
+// unit sees before the product reads them, and in rows that only some queries
+// see the elements that are not finite; where there was one, the softmax warps
+// add those elements to O of the rows that see them (a weight is positive: an
+// infinity stays itself, and NaN).  Such tiles are at most seven a unit (the
+// diagonal of 256 tokens, and the window's edge), so this takes the same time
+// behind any context, and what is added follows from the keys alone.
 //
 // What bounds it (148 SMs).  A step of two tiles takes the tensor cores 2048
 // cycles and ex2 2048, and one tile's chain (softmax 2000 - 2400, products
@@ -70,7 +73,7 @@ namespace pgd {
 
 constexpr uint32_t kLine = 128 * 128;         // bytes of a line: 128 rows x 128 B
 constexpr uint32_t kBox = 2 * kLine;          // [128 keys][128 dims], 16-bit
-constexpr int kRedoSlots = 8;
+constexpr int kBadSlots = 8;                  // units that a mark can be ahead
 constexpr uint32_t kMetaBytes = 1024;
 
 // Warps 0-7 are the softmax warpgroups; an FP8 cache takes more warps to
@@ -103,7 +106,7 @@ struct PrefillMeta {
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     Piece piece[kPieces];
     Share share;
-    uint32_t tmem, redo[kRedoSlots];
+    uint32_t tmem, bad[kBadSlots];   // units whose V had elements zeroed
 };
 static_assert(sizeof(PrefillMeta) <= kMetaBytes, "PrefillMeta grew");
 
@@ -146,9 +149,9 @@ __device__ __forceinline__ void piece_keys(const PrefillParams &p, Piece &u, int
 
 // ---------------------------------------------------------------- the V warps
 // Keep masked keys out of a 16-bit V box: zero the rows outside [lo, hi) of
-// the tile's keys, and tell whether one that only some query rows see, outside
-// [all_lo, all_hi), holds a non-finite value.  8 threads on one row's 128-byte
-// line.
+// the tile's keys, and the non-finite elements of rows that only some query
+// rows see, outside [all_lo, all_hi); tells whether there were any.  8 threads
+// on one row's 128-byte line.
 template <int WARPS>
 __device__ __forceinline__ bool clean_box(uint32_t box, int lo, int hi, int all_lo, int all_hi,
                                           int tid) {
@@ -162,12 +165,48 @@ __device__ __forceinline__ bool clean_box(uint32_t box, int lo, int hi, int all_
             sts128(a, 0, 0, 0, 0);
             sts128(a + kLine, 0, 0, 0, 0);
         } else {
-            uint32_t x[8];
+            uint32_t x[8], any = 0;
             lds128(a, x[0], x[1], x[2], x[3]);
             lds128(a + kLine, x[4], x[5], x[6], x[7]);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                bad |= (((x[k] & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u) != 0;
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t nf = ((x[k] & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u;
+                any |= nf;
+                x[k] &= ~((nf >> 15) * 0xFFFFu);
+            }
+            if (any) {
+                sts128(a, x[0], x[1], x[2], x[3]);
+                sts128(a + kLine, x[4], x[5], x[6], x[7]);
+                bad = true;
+            }
+        }
+    }
+    return bad;
+}
+
+// The same for the E4M3 rows of a box that is not converted yet: rows outside
+// [lo, hi) become zeros, and so do the NaN of the others (of rows that every
+// query sees too: one test less).  A thread takes the bytes that convert_box
+// has it read.
+template <int WARPS>
+__device__ __forceinline__ bool clean_bytes(uint32_t box, int lo, int hi, int tid) {
+    bool bad = false;
+#pragma unroll 1
+    for (int r = tid >> 3; r < 128; r += WARPS * 4) {
+        const uint32_t a = box + kLine + r * 128 + (((tid & 7) ^ (r & 7)) << 4);
+        uint32_t x[4], any = 0;
+        lds128(a, x[0], x[1], x[2], x[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t nan = ((x[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+            any |= nan;
+            x[k] &= ~((nan >> 7) * 0xFFu);
+        }
+        if (r < lo || r >= hi) {
+            sts128(a, 0, 0, 0, 0);
+        } else if (any) {
+            sts128(a, x[0], x[1], x[2], x[3]);
+            bad = true;
         }
     }
     return bad;
@@ -175,12 +214,10 @@ __device__ __forceinline__ bool clean_box(uint32_t box, int lo, int hi, int all_
 
 // An E4M3 box to f16, in place: a row's 128 bytes lie where the second half of
 // its 128 elements goes, and eight threads of one warp read the whole row
-// before they write it.  With `part`, as clean_box: rows outside [lo, hi)
-// become zeros unseen, and the others are looked at.
+// before they write it.
 template <int WARPS>
-__device__ __forceinline__ bool convert_box(uint32_t box, bool part, int lo, int hi, int tid) {
+__device__ __forceinline__ void convert_box(uint32_t box, int tid) {
     constexpr int U = 4;
-    bool bad = false;
     const int c = tid & 7, f = c >> 2, o = (c & 3) * 2;
 #pragma unroll 1
     for (int r0 = tid >> 3; r0 < 128; r0 += U * WARPS * 4) {
@@ -194,13 +231,6 @@ __device__ __forceinline__ bool convert_box(uint32_t box, bool part, int lo, int
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int r = r0 + u * WARPS * 4, sw = r & 7;
-            if (part) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (r < lo || r >= hi) x[u][k] = 0;
-                    bad |= (((x[u][k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-                }
-            }
             uint32_t y[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -221,7 +251,6 @@ __device__ __forceinline__ bool convert_box(uint32_t box, bool part, int lo, int
             }
         }
     }
-    return bad;
 }
 
 // A query row (eight threads of one warp, two 16-byte chunks each), bf16 ->
@@ -258,6 +287,45 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     float r;
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// Add the elements of V that the V warps zeroed, in the key tiles of this piece,
+// to O (at `o`) of the rows that see them; a row sees keys below `hi` (0: no
+// row).  One warp, all lanes alike; lane holds elements lane * D / 32 ...
+template <int D, bool FP8>
+__device__ __forceinline__ void add_bad_values(const PrefillParams &p, const Piece &u,
+                                            const TileKeys &tk, int hi, uint32_t o) {
+    constexpr int E = D / 32;
+    const ValueRows<D, FP8> rows(p, u.seq, u.h, u.kv0);
+#pragma unroll 1
+    for (int j = tk.kb; j < tk.ke; ++j) {
+        if (!is_partial(u, j)) continue;
+        const int end = min((j + 1) * kKeys, u.hi);
+#pragma unroll 1
+        for (int t = max(j * kKeys, u.lo); t < end; ++t) {
+            if (!FP8 && t >= u.all_lo && t < u.all_hi) continue;
+            float x[E];
+            const bool bad = rows.load(t, x);
+            const uint32_t found = __ballot_sync(0xffffffffu, bad);
+            const bool sees = t < hi && (p.window == 0 || hi - t <= p.window);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                if (!(found >> (c / E) & ((1u << 16 / E) - 1))) continue;
+                uint32_t y[16];
+                tmem_ld16(o + c, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    asm volatile("" : "+r"(y[i]));
+                    const float v = __shfl_sync(0xffffffffu, x[i % E], c / E + i / E);
+                    y[i] = sees && !(fabsf(v) < INFINITY)
+                               ? __float_as_uint(__uint_as_float(y[i]) + v) : y[i];
+                }
+                tmem_st16(o + c, y);
+                tmem_wait_st();
+            }
+        }
+    }
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -326,7 +394,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
             mbar_init(bar(meta.piece_full[i]), 1);
             mbar_init(bar(meta.piece_empty[i]), 1 + 4 * NQ + C::V_WARPS);   // MMA, softmax, V warps
         }
-        for (int i = 0; i < kRedoSlots; ++i) meta.redo[i] = 0;
+        for (int i = 0; i < kBadSlots; ++i) meta.bad[i] = 0;
         fence_mbar_init();
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
@@ -685,13 +753,15 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                     bool bad = false;
                     if (!wait(meta.full[s], (box / C::NS) & 1)) return false;
                     if (FP8 || part) {
-                        if (FP8)
-                            bad = convert_box<C::V_WARPS>(ring + s * kBox, part, lo, hi, tid);
-                        else
+                        if (FP8) {
+                            if (part) bad = clean_bytes<C::V_WARPS>(ring + s * kBox, lo, hi, tid);
+                            convert_box<C::V_WARPS>(ring + s * kBox, tid);
+                        } else {
                             bad = clean_box<C::V_WARPS>(ring + s * kBox, lo, hi, k.all_lo - j0,
                                                         k.all_hi - j0, tid);
+                        }
                         fence_proxy_async();
-                        if (bad) meta.redo[units % kRedoSlots] = units;
+                        if (bad) meta.bad[units % kBadSlots] = units;
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bar(meta.fixed[s]));
                     }
@@ -735,7 +805,6 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                 const bool valid = tok < tk.ntok;
                 const int hi = tk.p0 + tok + 1;
                 float m = -INFINITY, l = 0.f;
-                bool redo = false;
                 const bool any = tk.kb < tk.ke;
                 if (any) {
                     float mult = 0.f;
@@ -869,53 +938,11 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                     if (!(ok = wait(meta.o_done[t], done & 1))) break;
                     ++done;
                     tcgen05_fence_after();
-                    redo = reinterpret_cast<volatile uint32_t *>(meta.redo)[units % kRedoSlots] ==
-                           static_cast<uint32_t>(units);
+                    const uint32_t mark = reinterpret_cast<volatile uint32_t *>(meta.bad)[units % kBadSlots];
+                    if (__any_sync(0xffffffffu, mark == static_cast<uint32_t>(units)))
+                        add_bad_values<D, FP8>(p, u, tk, valid ? hi : 0, tmem + lanes + kOCol + t * 128);
                 }
                 const float vs = FP8 ? __ldg(p.v_scale + u.h) : 1.f;
-                if (redo) {
-                    KvRows kv;
-                    kv.flags = p.flags;
-                    kv.head = u.h; kv.hkv = p.num_kv_heads; kv.bs = p.block_size;
-                    kv.num_blocks = p.num_blocks;
-                    kv.row_bytes = FP8 ? D : 2 * D;
-                    kv.table = p.block_table ? p.block_table + static_cast<int64_t>(u.seq) * p.max_blocks_per_seq
-                                             : nullptr;
-                    kv.k_stride = p.k_stride * 2;
-                    kv.v_stride = p.v_stride * 2;
-                    const int64_t off = p.block_table ? 0 : static_cast<int64_t>(u.h) * D * 2;
-                    kv.k = static_cast<const uint8_t *>(p.k) + off + (p.block_table ? 0 : u.kv0 * kv.k_stride);
-                    kv.v = static_cast<const uint8_t *>(p.v) + off + (p.block_table ? 0 : u.kv0 * kv.v_stride);
-                    const float sl2 = p.scale * kLog2e * (FP8 ? __ldg(p.k_scale + u.h) : 1.f);
-                    for (int rr = 0; rr < 32; ++rr) {
-                        const int ro = __shfl_sync(0xffffffffu, r, rr);
-                        const int tk_i = ro / g, hd_i = ro - tk_i * g;
-                        if (tk_i >= tk.ntok) continue;
-                        const int h1 = tk.p0 + tk_i + 1;
-                        const int a = max(p.window > 0 ? max(0, h1 - p.window) : 0, tk.kb * kKeys);
-                        const int b = min(h1, tk.ke * kKeys);
-                        const int64_t tr = u.row0 + t * tpq + tk_i;
-                        const int q1 = u.h * g + hd_i;
-                        float acc[D / 32], mm, ll;
-                        attend_row<D, FP8>(p.q + tr * p.q_stride + q1 * D, kv, a, b, sl2, acc, mm, ll);
-                        const float inv = ll == 0.f ? 0.f : vs / ll;
-                        const int64_t orow = tr * p.num_q_heads + q1;
-                        if (u.slot >= 0) {
-                            const int64_t pr = (static_cast<int64_t>(u.slot) * NQ + t) * 128 + ro;
-                            for (int i = 0; i < D / 32; ++i)
-                                p.o_part[pr * D + lane * (D / 32) + i] = acc[i] * inv;
-                            if (lane == 0)
-                                p.lse_part[pr] = ll == 0.f ? -INFINITY : mm * 0.6931471805599453f + logf(ll);
-                        } else {
-                            uint32_t *o = reinterpret_cast<uint32_t *>(p.out + orow * D) + lane * (D / 64);
-                            for (int i = 0; i < D / 64; ++i)
-                                o[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-                            if (p.lse_out && lane == 0)
-                                p.lse_out[orow] = ll == 0.f ? -INFINITY : mm * 0.6931471805599453f + logf(ll);
-                        }
-                    }
-                    continue;
-                }
                 const bool dead = l == 0.f;
                 const float inv = dead ? 0.f : vs / l;
                 const float lse = dead ? -INFINITY : m * 0.6931471805599453f + logf(l);

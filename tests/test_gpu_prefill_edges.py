@@ -1,10 +1,13 @@
 """Prompt attention at the edges of its tiles, shares and number ranges, against
 the definition in 64 bits (tests/prefill_ref.py derives the tolerances)."""
+import math
+
 import pytest
 import torch
 
 import paged_gqa_decode_07_b200 as pgd
-from tests.test_gpu_prefill import check_packed, check_paged
+from tests.test_gpu_prefill import (bits, check_packed, check_paged, cu_of, make_pages, randn,
+                                    run_packed, run_paged)
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +59,108 @@ def test_more_ctas_than_the_axis_is_long(d, dt, ctas):
     if dt == "bf16":
         check_packed([200], 1, 1, d, seed=312, num_ctas=ctas,
                      workspace=nan_workspace(1, 200, 200, 1, 1, d, ctas))
+
+
+# --------------------------------------------------------------------------- #
+# Values that are not finite                                                  #
+# --------------------------------------------------------------------------- #
+def paged_case(ctx, q_lens, hq, hkv, d, bs, dt, seed):
+    kc, vc, table, ks, vs = make_pages(ctx, hkv, d, bs, dt, seed)
+    cu, cu_t = cu_of(q_lens)
+    q = randn((cu[-1], hq, d), seed + 9)
+
+    def run(v_cache, **kw):
+        return run_paged(q, kc, v_cache, table, ctx, cu_t, hq, hkv, d, bs, 1 / math.sqrt(d), ks,
+                         vs, max_context_len=max(ctx), **kw)
+
+    def spoil(places):
+        """V with the values of {(sequence, position, head, element): x}."""
+        bad = vc.clone()
+        for (s, t, h, e), x in places.items():
+            bad[table[s, t // bs].long(), h, t % bs, e] = 0x7F if dt == "e4m3" else x
+        return bad
+    return run, vc, spoil, cu
+
+
+def assert_only_there(got, clean, spoiled):
+    """Bits as with a finite value, but for the outputs `spoiled` [T][Hq][D],
+    which are not finite."""
+    out, lse = got
+    assert torch.equal(bits(lse), bits(clean[1]))
+    assert torch.equal(bits(out)[~spoiled], bits(clean[0])[~spoiled])
+    assert not bool(torch.isfinite(out[spoiled]).any())
+
+
+@pytest.mark.parametrize("ctas", [0, 1], ids=["auto", "one"])
+@pytest.mark.parametrize("d,dt", [(128, "bf16"), (256, "bf16"), (128, "e4m3")])
+def test_a_newest_value_that_is_not_finite_behind_a_long_context(d, dt, ctas):
+    """It reaches the newest rows alone, and takes no time that grows with the
+    context: nothing gives up waiting, and the work behind it is done."""
+    ctx, q_lens = [150001, 70, 90], [5, 70, 3]
+    run, vc, spoil, cu = paged_case(ctx, q_lens, 4, 1, d, 64, dt, 400)
+    clean = run(vc, num_ctas=ctas)
+    got = run(spoil({(0, 149999, 0, 3): math.nan, (0, 149999, 0, d - 1): math.nan}),
+              num_ctas=ctas)
+    assert pgd.get_device_error() == 0
+    spoiled = torch.zeros(clean[0].shape, dtype=torch.bool, device="cuda")
+    spoiled[3:5, :, [3, d - 1]] = True           # positions 149999 and 150000
+    assert_only_there(got, clean, spoiled)
+
+
+@pytest.mark.parametrize("d,dt", [(128, "bf16"), (256, "bf16"), (128, "e4m3")])
+@pytest.mark.parametrize("window", [0, 1, 77, 300])
+def test_many_values_that_are_not_finite(d, dt, window):
+    """Every row sees its own ones: behind the causal mask, at the window's
+    edge, in every element of a row, in cut pieces; the same bits each time."""
+    n, hq, hkv = 611, 2, 1
+    run, vc, spoil, cu = paged_case([n, 9], [600, 1], hq, hkv, d, 32, dt, 410)
+    g = torch.Generator().manual_seed(5)
+    places = {}
+    for x in (math.nan, math.inf, -math.inf):
+        for t in torch.randint(0, n, (6,), generator=g).tolist():
+            places[(0, t, 0, int(torch.randint(0, d, (1,), generator=g)))] = x
+    places.update({(0, n - 1, 0, e): math.inf for e in range(d)})
+    pos = torch.arange(n - 600, n, device="cuda")
+    spoiled = torch.zeros((601, hq, d), dtype=torch.bool, device="cuda")
+    for (_, t, _, e) in places:
+        sees = (pos >= t) & ((pos < t + window) if window else (pos >= t))
+        spoiled[:600, :, e] |= sees[:, None]
+    for ctas in (1, 3, 20):
+        clean = run(vc, window=window, num_ctas=ctas)
+        v = spoil(places)
+        first = run(v, window=window, num_ctas=ctas)
+        assert_only_there(first, clean, spoiled)
+        for _ in range(3):
+            again = run(v, window=window, num_ctas=ctas)
+            for a, b in zip(first, again):
+                assert torch.equal(bits(a), bits(b))
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_infinities_keep_their_sign(d):
+    """In tiles that only some rows see, packed."""
+    n, hq = 300, 2
+    q, k, v = (randn((n, h, d), 420 + i) for i, h in enumerate((hq, 1, 1)))
+    cu, cu_t = cu_of([n])
+    v[280, 0, 7], v[285, 0, 7], v[290, 0, 9], v[280, 0, d - 2] = math.inf, -math.inf, -math.inf, 1
+    out, _ = run_packed(q, k, v, cu_t, hq, 1, d, 0.09)
+    assert bool(torch.isfinite(out[:280]).all())
+    assert bool((out[280:285, :, 7] == math.inf).all())
+    assert bool(torch.isnan(out[285:, :, 7]).all())
+    assert bool((out[290:, :, 9] == -math.inf).all()) and bool(torch.isfinite(out[:290, :, 9]).all())
+
+
+@pytest.mark.parametrize("ctas", [0, 2])
+def test_a_bad_value_that_only_the_second_query_tile_sees(ctas):
+    """The first tile's rows keep the bits that they have without it, whichever
+    warp comes first."""
+    n, hq, d = 256, 1, 128                       # one unit: two tiles of 128 tokens
+    q, k, v = (randn((n, h, d), 430 + i) for i, h in enumerate((hq, 1, 1)))
+    cu_t = cu_of([n])[1]
+    clean = run_packed(q, k, v, cu_t, hq, 1, d, 0.09, num_ctas=ctas)
+    v[200, 0, 11] = math.nan
+    spoiled = torch.zeros((n, hq, d), dtype=torch.bool, device="cuda")
+    spoiled[200:, :, 11] = True
+    for _ in range(30):
+        got = run_packed(q, k, v, cu_t, hq, 1, d, 0.09, num_ctas=ctas)
+        assert_only_there(got, clean, spoiled)
