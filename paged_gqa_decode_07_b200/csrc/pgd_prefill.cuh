@@ -124,9 +124,9 @@ __device__ __forceinline__ bool is_partial(const Piece &k, int j) {
 template <int NQ>
 __device__ __forceinline__ void piece_keys(const PrefillParams &p, Piece &u, int tpq) {
     u.hi = u.pos0 + u.ntok;
-    u.lo = p.window > 0 ? max(0, u.pos0 + 1 - p.window) : 0;
+    u.lo = first_seen(p, u.pos0);
     u.all_hi = u.pos0 + 1;
-    u.all_lo = p.window > 0 ? u.hi - p.window : 0;
+    u.all_lo = first_seen(p, u.hi - 1);
     u.part_lo = 0;
     u.part_hi = 0x7fffffff;
 #pragma unroll
@@ -137,9 +137,9 @@ __device__ __forceinline__ void piece_keys(const PrefillParams &p, Piece &u, int
         t.kb = t.ke = t.mlo = t.mhi = 0;
         const int hi = t.p0 + t.ntok;
         if (t.ntok > 0 && hi > 0) {
-            t.kb = max(p.window > 0 ? max(0, t.p0 + 1 - p.window) / kKeys : 0, u.kb);
+            t.kb = max(first_seen(p, t.p0) / kKeys, u.kb);
             t.ke = max(t.kb, min((hi + kKeys - 1) / kKeys, u.ke));
-            t.mlo = p.window > 0 ? (max(0, hi - p.window) + kKeys - 1) / kKeys : 0;
+            t.mlo = (first_seen(p, hi - 1) + kKeys - 1) / kKeys;
             t.mhi = max(0, t.p0 + 1) / kKeys;
             u.part_lo = max(u.part_lo, t.mlo);
             u.part_hi = min(u.part_hi, t.mhi);
@@ -827,7 +827,7 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                             // -inf, and all of them negated for a negative scale;
                             // columns [b, a) are the row's
                             const int a = masked ? hi - j * kKeys : kKeys;
-                            const int b = masked && p.window > 0 ? hi - p.window - j * kKeys : 0;
+                            const int b = masked ? first_seen(p, hi - 1) - j * kKeys : 0;
 #pragma unroll 1
                             for (int c = 0; c < 128; c += 32) {
                                 if (!__any_sync(0xffffffffu, mult < 0.f || a < c + 32 || b > c)) continue;

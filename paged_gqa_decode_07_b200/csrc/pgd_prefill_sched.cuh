@@ -181,6 +181,12 @@ __device__ void find_share(const PrefillParams &p, Share &share) {
     }
 }
 
+// The first position that a row at position `pos` sees (of those from 0 on);
+// `pos` may be negative and the window anything up to 2^31 - 1.
+__device__ __forceinline__ int first_seen(const PrefillParams &p, int pos) {
+    return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+}
+
 // A whole unit of a sequence from its token tok0 on; its key tiles as [kb, ke),
 // one empty tile for a unit that sees nothing.
 __device__ __forceinline__ void unit_piece(const PrefillParams &p, const SeqRows &s, int seq, int h,
@@ -193,7 +199,7 @@ __device__ __forceinline__ void unit_piece(const PrefillParams &p, const SeqRows
     u.kv0 = s.row;
     u.slot = -1;
     hi = max(0, u.pos0 + u.ntok);
-    lo = p.window > 0 && hi > 0 ? max(0, u.pos0 + 1 - p.window) : 0;
+    lo = hi > 0 ? first_seen(p, u.pos0) : 0;
     u.kb = lo / kKeys;
     u.ke = max(u.kb + 1, (hi + kKeys - 1) / kKeys);
 }

@@ -164,3 +164,25 @@ def test_a_bad_value_that_only_the_second_query_tile_sees(ctas):
     for _ in range(30):
         got = run_packed(q, k, v, cu_t, hq, 1, d, 0.09, num_ctas=ctas)
         assert_only_there(got, clean, spoiled)
+
+
+# --------------------------------------------------------------------------- #
+# The largest windows                                                         #
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("window", [1 << 30, (1 << 31) - 2, (1 << 31) - 1])
+@pytest.mark.parametrize("d,dt", [(128, "bf16"), (256, "bf16"), (128, "e4m3")])
+def test_windows_longer_than_any_context(d, dt, window):
+    """Rows at negative positions see nothing, and the others what they see
+    without a window, whatever the window's size."""
+    q_lens, ctx = [130, 300, 64, 1], [3, 120, 0, 700]
+    for ctas in (0, 1, 3, 40):
+        kw = dict(seed=320, num_ctas=ctas, gap=1, tail=2)
+        want = check_paged(q_lens, ctx, 6, 2, d, 16, dt, **kw)
+        got = check_paged(q_lens, ctx, 6, 2, d, 16, dt, window=window, **kw)
+        for a, b in zip(want, got):
+            assert torch.equal(bits(a), bits(b))
+    if dt == "bf16":
+        want = check_packed([400, 1], 6, 2, d, seed=321)
+        got = check_packed([400, 1], 6, 2, d, seed=321, window=window)
+        for a, b in zip(want, got):
+            assert torch.equal(bits(a), bits(b))
