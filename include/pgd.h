@@ -358,8 +358,9 @@ pgd_status pgd_prefill_attention(const void *q, int64_t q_stride, const void *k,
  *                sees are not read.  head_dim 256 with bf16 only
  *   max_q_len, max_context_len  host hints >= every L and n (0 = unknown);
  *                only used to choose whether work is cut
- * With an FP8 cache the weights enter the second product as f16 (half a step:
- * 2^-11).
+ * With an FP8 cache the weights enter the second product as f16: half a step
+ * is 2^-11 of a weight down to 2^-21 of the row's largest, and 2^-32 of the
+ * largest for smaller ones.
  */
 pgd_status pgd_paged_prefill_attention(
     const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,

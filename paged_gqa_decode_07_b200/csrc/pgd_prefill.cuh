@@ -36,7 +36,10 @@
 // are p = 2^(x - m), and m moves (O and l rescaled) only when a score exceeds
 // it by more than 8 (weights stay below 2^8, O below 2^8 times its value).
 // P enters the product as bf16 (f16 for FP8 caches, whose V is exact there);
-// l sums the unrounded weights.
+// l sums the unrounded weights.  f16 ends at 2^-25: there m is put 7 below the
+// maximum, weights reach up to 2^15, and what rounds to zero is below 2^-32 of
+// the largest (2^-25 before: n * 2^-25 of the result was lost behind one
+// dominant key, with 262144 keys 2^-7).
 //
 // Masked keys.  A masked weight is zero, but zero times a value that is not
 // finite is NaN, and rows of unowned slots may hold anything.  On key tiles
@@ -869,9 +872,10 @@ prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillParams p) 
                         const float am = fabsf(mult);
                         const float top = valid ? mx * am : -INFINITY;
                         // also for NaN, which poisons the row's sum, and +inf
-                        const bool move = !(top <= m + 8.f);
+                        constexpr float kBelow = FP8 ? 7.f : 0.f;
+                        const bool move = !(top <= m + (8.f + kBelow));
                         if (__any_sync(0xffffffffu, move)) {
-                            const float m_new = move ? top : m;
+                            const float m_new = move ? top - kBelow : m;
                             float alpha = move ? ex2(m - m_new) : 1.f;
                             m = m_new;
                             alpha = top < INFINITY ? alpha : NAN;

@@ -186,3 +186,47 @@ def test_windows_longer_than_any_context(d, dt, window):
         got = check_packed([400, 1], 6, 2, d, seed=321, window=window)
         for a, b in zip(want, got):
             assert torch.equal(bits(a), bits(b))
+
+
+# --------------------------------------------------------------------------- #
+# Many small weights behind one large one                                     #
+# --------------------------------------------------------------------------- #
+def dominant_key(n, log2_weight, d, bs, dt):
+    """A cache of n rows: the first weighs 1 and its value is zero, the others
+    weigh 2^-log2_weight and their values are one.  Returns q, caches, table,
+    softmax scale, scales."""
+    nb = -(-n // bs)
+    if dt == "e4m3":
+        kc, vc = (torch.full((nb, 1, bs, d), x, device="cuda").to(torch.float8_e4m3fn)
+                  for x in (0.0, 1.0))
+        one = torch.ones(1, device="cuda")
+        scales = (one, one)
+    else:
+        kc, vc = (torch.full((nb, 1, bs, d), x, dtype=torch.bfloat16, device="cuda")
+                  for x in (0.0, 1.0))
+        scales = (None, None)
+    kc[..., 0] = -16.0
+    kc[0, 0, 0, 0] = 0
+    vc[0, 0, 0] = 0
+    table = torch.arange(nb, dtype=torch.int32, device="cuda")[None, :].contiguous()
+    q = torch.zeros((1, 4, d), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    if dt == "e4m3":
+        kc, vc = kc.view(torch.uint8), vc.view(torch.uint8)
+    return q, kc, vc, table, log2_weight * math.log(2) / 16, scales
+
+
+@pytest.mark.parametrize("ctas", [1, 0], ids=["one", "auto"])
+@pytest.mark.parametrize("e", [14.3, 18.3, 21.3, 24.3, 26.3, 28.3])
+def test_small_weights_of_an_fp8_cache_are_not_lost(e, ctas):
+    """o = n w / (1 + n w).  Each weight is off by half a step of f16 (2^-11) or
+    2^-32 of the largest, the output by half a step, the two sums of n terms by
+    2^-23 a term, and the scores by 2^-21 of their size."""
+    n, bs = 262145, 64
+    q, kc, vc, table, scale, (ks, vs) = dominant_key(n, e, 128, bs, "e4m3")
+    out, _ = run_paged(q, kc, vc, table, [n], cu_of([1])[1], 4, 1, 128, bs, scale, ks, vs,
+                       max_context_len=n, num_ctas=ctas)
+    w = (n - 1) * 2.0 ** -e
+    o = w / (1 + w)
+    tol = o * (2.0 ** -8 + 2.0 ** -11 + 2 * n * 2.0 ** -23 + e * 2.0 ** -21) + n * 2.0 ** -32
+    assert bool(((out.double() - o).abs() <= tol).all()), (float(out[0, 0, 0]), o, tol)
