@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps, 2) prefill_merge_kernel(cons
                 }
 #pragma unroll
                 for (int z = 0; z < R; ++z) {
+                    // also for a weight of zero: a piece that is not finite stays so
                     const float f = __shfl_sync(0xffffffffu, w, z * PB + at);
-                    if (f == 0.f) continue;
 #pragma unroll
                     for (int k = 0; k < E4; ++k) {
                         acc[z][k].x += f * o[z][k].x; acc[z][k].y += f * o[z][k].y;

@@ -230,3 +230,26 @@ def test_small_weights_of_an_fp8_cache_are_not_lost(e, ctas):
     o = w / (1 + w)
     tol = o * (2.0 ** -8 + 2.0 ** -11 + 2 * n * 2.0 ** -23 + e * 2.0 ** -21) + n * 2.0 ** -32
     assert bool(((out.double() - o).abs() <= tol).all()), (float(out[0, 0, 0]), o, tol)
+
+
+# --------------------------------------------------------------------------- #
+# Pieces of no weight                                                         #
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("late", [False, True], ids=["before", "behind"])
+@pytest.mark.parametrize("d,dt", [(128, "bf16"), (256, "bf16"), (128, "e4m3")])
+def test_a_nan_in_a_piece_whose_weight_vanishes(d, dt, late):
+    """Keys of one half score 300 more than the others: e^-300 is zero in fp32.
+    A NaN that a row sees there shows, whether the work is cut or not."""
+    n, bs = 2048, 16
+    q, kc, vc, table, scale, (ks, vs) = dominant_key(n, 300 / math.log(2), d, bs, dt)
+    zero, nan = (0, 0x7F) if dt == "e4m3" else (0.0, math.nan)
+    half = slice(0, n // 2 // bs) if late else slice(n // 2 // bs, None)
+    kc[half, ..., 0] = zero                      # the half that weighs
+    at = n * 3 // 4 if late else n // 4
+    vc[at // bs, 0, at % bs, 5] = nan
+    for ctas in (1, 2, 5, 40):
+        out, lse = run_paged(q, kc, vc, table, [n], cu_of([1])[1], 4, 1, d, bs, scale, ks, vs,
+                             num_ctas=ctas)
+        assert bool(torch.isnan(out[..., 5]).all()), f"{ctas} CTAs"
+        keep = torch.arange(d, device="cuda") != 5
+        assert bool(torch.isfinite(out[..., keep]).all()) and bool(torch.isfinite(lse).all())
