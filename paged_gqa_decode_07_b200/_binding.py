@@ -610,9 +610,14 @@ def _prefill_workspace(workspace, need: int, device, stream):
 
 @functools.lru_cache(maxsize=256)
 def _prefill_need(device: int, *sizes: int) -> int:
-    """pgd_prefill_workspace_bytes on the current device (a function of the
-    sizes and the device alone)."""
-    return int(load_library().pgd_prefill_workspace_bytes(*sizes))
+    """pgd_prefill_workspace_bytes on the current device, asked once per shape
+    (a function of the sizes and the device alone).  An error is raised and
+    not kept: 0 means "does not cut" or an error, and two CTAs always cut."""
+    ask = load_library().pgd_prefill_workspace_bytes
+    need = int(ask(*sizes))
+    if need == 0 and ask(1, 1, 1, 0, 1, 1, 128, 2) == 0:
+        raise PGDError(3, "pgd_prefill_workspace_bytes")      # a CUDA call failed
+    return need
 
 
 def prefill_workspace_bytes(num_seqs: int, num_tokens: int, max_context_len: int, window: int,

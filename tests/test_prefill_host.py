@@ -170,3 +170,33 @@ def test_packed_reference_is_causal_softmax():
         want = torch.nn.functional.scaled_dot_product_attention(
             q[a:b].transpose(0, 1), kk, vv, is_causal=True, scale=0.3)
         torch.testing.assert_close(out[a:b].transpose(0, 1), want, rtol=1e-10, atol=1e-12)
+
+
+class _Sizes:
+    """pgd_prefill_workspace_bytes of a device that cannot be asked at first."""
+
+    def __init__(self, answer):
+        self.answer, self.fails, self.asked = answer, True, 0
+
+    def pgd_prefill_workspace_bytes(self, seqs, tokens, keys, window, hq, hkv, d, ctas):
+        self.asked += 1
+        if self.fails:
+            return 0
+        return 4096 if ctas == 2 else self.answer
+
+
+@pytest.mark.parametrize("answer", [1 << 20, 0], ids=["cut", "whole"])
+def test_a_workspace_size_that_failed_is_asked_again(monkeypatch, answer):
+    from paged_gqa_decode_07_b200 import _binding
+    lib = _Sizes(answer)
+    monkeypatch.setattr(_binding, "load_library", lambda: lib)
+    _binding._prefill_need.cache_clear()
+    sizes = (99, 3, 5000, 4000, 0, 8, 2, 128, 0)
+    with pytest.raises(_binding.PGDError):
+        _binding._prefill_need(*sizes)
+    lib.fails = False
+    assert _binding._prefill_need(*sizes) == answer
+    asked = lib.asked
+    assert _binding._prefill_need(*sizes) == answer
+    assert lib.asked == asked, "an answer is kept"
+    _binding._prefill_need.cache_clear()
