@@ -112,3 +112,31 @@ def test_an_output_made_on_another_stream_outlives_its_reader():
     assert after.data_ptr() != at
     torch.cuda.synchronize()
     assert torch.equal(bits(got), bits(want))
+
+
+@pytest.mark.parametrize("side", [False, True], ids=["captured", "joined"])
+def test_a_captured_call_that_names_its_stream(side):
+    """The capturing stream itself, or one that the capture forks to and joins;
+    the output and the workspace are made inside the call."""
+    n = 1500
+    cu_t = cu_of([n])[1]
+    q, k, v = prompts(n, 50)
+    pgd.prefill_attention(q, k, v, cu_t, HQ, HKV, D, 0.09, num_ctas=9)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cur = torch.cuda.current_stream()
+        on = s if side else cur
+        if side:
+            s.wait_stream(cur)
+        out = pgd.prefill_attention(q, k, v, cu_t, HQ, HKV, D, 0.09, num_ctas=9, stream=on)
+        if side:
+            cur.wait_stream(s)
+    for seed in (60, 70):
+        for t, x in zip((q, k, v), prompts(n, seed)):
+            t.copy_(x)
+        g.replay()
+        want = pgd.prefill_attention(q, k, v, cu_t, HQ, HKV, D, 0.09, num_ctas=9)
+        torch.cuda.synchronize()
+        assert torch.equal(bits(out), bits(want))
