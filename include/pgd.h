@@ -290,7 +290,8 @@ pgd_status pgd_paged_decode_attention_ex(
  *   lse = M + ln sum_t exp(x_t - M)
  * over the visible positions t: t <= i, and with window > 0 also
  * t > i - window.  A key that a row does not see has no influence on it, not
- * even if it holds infinities or NaN.
+ * even if it holds infinities or NaN; an element of V that is not finite makes
+ * that element of the rows that see it not finite.
  *
  *   q            device bf16, row i at q + i * q_stride: [num_q_heads][head_dim]
  *   k, v         device bf16, row i at k + i * k_stride (v + i * v_stride):
@@ -323,7 +324,9 @@ pgd_status pgd_paged_decode_attention_ex(
  *                call returns PGD_ERR_WORKSPACE
  *   stream       cudaStream_t as void*
  * Weights enter the second product as bf16 (half a step: 2^-8 of each weight)
- * and the normaliser sums them in fp32 before that rounding.  Repeated calls
+ * and the normaliser sums them in fp32 before that rounding.  (The decode calls
+ * give a weight two bf16 terms: a sequence that moves between them and this one
+ * is rounded differently.)  Repeated calls
  * with the same inputs and num_ctas give the same bits.  num_seqs = 0 or
  * num_tokens = 0 enqueues nothing.
  */
@@ -458,8 +461,9 @@ pgd_decode_math pgd_get_decode_math(void);
 /* Test hook for the timeout path                                           */
 /* ------------------------------------------------------------------------ */
 /*
- * Every wait inside the decode kernels (a K/V stage landing, a segment
- * descriptor, a free ring slot, an appended row) is bounded: after the limit
+ * Every wait inside the decode and prompt attention kernels (a K/V stage
+ * landing, a segment descriptor or piece, a free ring slot, an appended row, a
+ * product or its weights) is bounded: after the limit
  * the kernel raises the timeout flag (8), its warps leave together, the
  * producer still waits for every copy it issued (with its own fixed limit of
  * 1 s) so nothing lands after the CTA exits, and pgd_get_device_error()
@@ -468,7 +472,7 @@ pgd_decode_math pgd_get_decode_math(void);
  * exists to test that path: a limit of a few ns makes the waits give up.
  *
  * pgd_debug_set_wait_limit_ns -- process-wide limit of those waits for the
- * decode launches that follow, in ns; 0 restores the default (1 s).  Outputs
+ * attention launches that follow, in ns; 0 restores the default (1 s).  Outputs
  * of a launch that timed out are undefined.  Not for production use.
  * pgd_debug_get_wait_limit_ns -- the current limit.
  */

@@ -426,7 +426,7 @@ def get_decode_math() -> str:
 
 
 def debug_set_wait_limit_ns(limit_ns: int) -> None:
-    """Limit of the decode kernels' pipeline waits, in ns, for the launches
+    """Limit of the attention kernels' pipeline waits, in ns, for the launches
     that follow (pgd_debug_set_wait_limit_ns); 0 restores the default 1 s.
     A test hook for the timeout path."""
     _check(load_library().pgd_debug_set_wait_limit_ns(int(limit_ns)),

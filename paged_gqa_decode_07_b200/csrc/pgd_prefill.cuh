@@ -35,8 +35,9 @@
 // Softmax, one pass with a running reference m and sum l in fp32: the weights
 // are p = 2^(x - m), and m moves (O and l rescaled) only when a score exceeds
 // it by more than 8 (weights stay below 2^8, O below 2^8 times its value).
-// P enters the product as bf16 (f16 for FP8 caches, whose V is exact there);
-// l sums the unrounded weights.  f16 ends at 2^-25: there m is put 7 below the
+// P enters the product as bf16 (f16 for FP8 caches, whose V is exact there):
+// both operands have one type, and a second term for the lost bits would double
+// the P V products.  l sums the unrounded weights.  f16 ends at 2^-25: there m is put 7 below the
 // maximum, weights reach up to 2^15, and what rounds to zero is below 2^-32 of
 // the largest (2^-25 before: n * 2^-25 of the result was lost behind one
 // dominant key, with 262144 keys 2^-7).
@@ -54,8 +55,9 @@
 // What bounds it (148 SMs).  A step of two tiles takes the tensor cores 2048
 // cycles and ex2 2048, and one tile's chain (softmax 2000 - 2400, products
 // 1330) leaves both busy 0.55 - 0.6 of the time.  64 heads over 8, 8192 tokens:
-// 980 - 1040 us, 1.06 - 1.12 PFLOP/s at the power cap (992 W, 1.74 GHz), where
-// plain matrix products sustain 1.39.  Every instruction of the MMA warp
+// 975 - 1040 us by itself (1.06 - 1.13 PFLOP/s), 1120 - 1135 in calls one after
+// another on changing inputs, at the power cap (992 W, 1.74 GHz), where plain
+// matrix products sustain 1.39 PFLOP/s.  Every instruction of the MMA warp
 // counts: descriptors built per product (18 instructions each by the code's
 // size, 4 now), branches and 64-bit compares before a wait and conditions in
 // the loop cost 5400 cycles a step, the straight form 3700.

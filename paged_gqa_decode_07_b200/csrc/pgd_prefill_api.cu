@@ -43,15 +43,28 @@ pgd_status check_common(int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
 }
 
 // Units are cut from this many keys on (the host's bound on what a unit's rows
-// see).  Whole / cut, us, 32 heads over 8 of 128: one new token after 768 keys
-// 18.0 / 19.4, 1280: 25.7 / 22.1, 2048: 36.9 / 26.6; a prompt of 1024 26.6 /
-// 35.1, 1280: 45.4 / 42.4, 1792: 60.6 / 51.7; four prompts 42.5 / 57.1, 70.2 /
-// 68.9, 110.4 / 107.7; 8192 tokens with a window of 1024 163 / 180.
+// see).  Cutting evens out what the longest unit would take alone (about 1 us
+// per 128 keys) and costs the merge, 9 - 14 us with caches flushed.  Whole /
+// cut in us, caches flushed:
+//   keys               1024         1280         1536         2048
+//   32 heads over 8 of 128, bf16
+//     one new token    26.7 / 25.6  30.8 / 27.7  34.8 / 27.8  41.1 / 33.8
+//     a prompt         30.8 / 39.9  49.2 / 48.2  61.5 / 54.3  69.7 / 70.7
+//     four prompts     65.6 / 76.8  90 / 101     115 / 126    174 / 185
+//   32 heads over 8 of 128, E4M3
+//     one new token    33.8 / 33.8  37.9 / 33.9  42.0 / 35.8  52.2 / 39.9
+//     a prompt         42.0 / 52.2  67.6 / 64.5  76.7 / 64.5  84.0 / 80.9
+//     four prompts     82.0 / 91.2  110 / 120    141 / 150    207 / 220
+//   32 heads over 4 of 256, bf16
+//     one new token    41.0 / 27.6  49.2 / 27.6  55.4 / 29.6  71.7 / 31.7
+//     a prompt         43.1 / 52.3  57.4 / 62.3  71.7 / 72.7  111 / 99.3
+//     four prompts     100 / 116    141 / 148    178 / 192    276 / 292
+// Single tokens gain, equal prompts lose up to a tenth; the host's bounds do
+// not tell them apart.
 constexpr int64_t kCutKeys = 1280;
 
 // Grid, and whether units are cut: one CTA per SM, one per unit where they
-// stay whole.  Cutting costs the merge kernel (about 4 us) and evens out
-// what the longest unit would take alone (about 1 us per 128 keys).
+// stay whole.
 struct PrefillPlan {
     int grid;
     bool cut;

@@ -23,9 +23,17 @@ namespace pgd {
 
 constexpr int kMaxThreads = 512;
 constexpr int kKeys = 128;           // keys per tile
-// A unit's fixed cost, in keys.  One prompt of 8192 tokens and a ragged batch:
-// 128: 1071 and 225 us, 256: 1010 and 190, 384: 999 and 190, 512: 990 and 199,
-// 768: 1019 and 214.
+// A unit's fixed cost, in keys.  Times in us, caches flushed:
+//                                          128   256   384   512   768
+//   bf16 D 128: prompt of 8192 (64/8)     1022   962   975   986  1015
+//               ragged prompts (32/8)      193   170   174   182   194
+//               mixed step (32/8)          117   112   114   117   123
+//   bf16 D 256: prompt of 4096 (32/2)      367   292   258   263   266
+//               ragged prompts (32/4)      367   307   279   291   302
+//               mixed step (32/4)          166   155   160   166   172
+//   E4M3 D 128: prompt of 4096 (32/8)      215   195   186   186   199
+//               ragged prompts (32/8)      247   220   209   215   227
+//               mixed step (32/8)          150   131   129   125   135
 constexpr int kUnitKeys = 384;
 constexpr int kPieces = 4;           // pieces handed out ahead
 
