@@ -133,7 +133,9 @@ class Prepared:
     more host time than a small batch's kernel takes on the GPU.  Calling a
     Prepared object re-issues the C call with the pointers, sizes and stream
     it was prepared with and returns what the original call returned.  The
-    tensors must stay alive and keep their storage while it is in use."""
+    tensors must stay alive and keep their storage while it is in use, and so
+    must the object itself where a graph captured its call: it holds the
+    workspace that the binding allocated."""
 
     __slots__ = ("_fn", "_args", "_name", "result", "_keep")
 

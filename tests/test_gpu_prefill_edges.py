@@ -253,3 +253,18 @@ def test_a_nan_in_a_piece_whose_weight_vanishes(d, dt, late):
         assert bool(torch.isnan(out[..., 5]).all()), f"{ctas} CTAs"
         keep = torch.arange(d, device="cuda") != 5
         assert bool(torch.isfinite(out[..., keep]).all()) and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("d,dt", [(128, "bf16"), (256, "bf16"), (128, "e4m3")])
+@pytest.mark.parametrize("window", [0, 300])
+def test_no_value_is_finite(d, dt, window):
+    """Every element of every tile, with a window of which no tile is seen
+    whole: the longest that a unit can take over them, in one CTA too."""
+    ctx, q_lens = [3000, 200], [3000, 1]
+    run, vc, _, cu = paged_case(ctx, q_lens, 2, 2, d, 16, dt, 440)
+    bad = torch.full_like(vc, 0x7F if dt == "e4m3" else math.nan)
+    for ctas in (0, 1):
+        clean = run(vc, window=window, num_ctas=ctas)
+        out, lse = run(bad, window=window, num_ctas=ctas)
+        assert pgd.get_device_error() == 0
+        assert bool(torch.isnan(out).all()) and torch.equal(bits(lse), bits(clean[1]))
