@@ -37,10 +37,10 @@
 // it by more than 8 (weights stay below 2^8, O below 2^8 times its value).
 // P enters the product as bf16 (f16 for FP8 caches, whose V is exact there):
 // both operands have one type, and a second term for the lost bits would double
-// the P V products.  l sums the unrounded weights.  f16 ends at 2^-25: there m is put 7 below the
-// maximum, weights reach up to 2^15, and what rounds to zero is below 2^-32 of
-// the largest (2^-25 before: n * 2^-25 of the result was lost behind one
-// dominant key, with 262144 keys 2^-7).
+// the P V products.  l sums the unrounded weights.  f16 ends at 2^-25: there m
+// is put 7 below the maximum, weights reach up to 2^15, and what rounds to zero
+// is below 2^-32 of the largest (2^-25 before: n * 2^-25 of the result was lost
+// behind one dominant key, with 262144 keys 2^-7).
 //
 // Masked keys.  A masked weight is zero, but zero times a value that is not
 // finite is NaN, and rows of unowned slots may hold anything.  On key tiles
@@ -299,7 +299,7 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // row).  One warp, all lanes alike; lane holds elements lane * D / 32 ...
 template <int D, bool FP8>
 __device__ __forceinline__ void add_bad_values(const PrefillParams &p, const Piece &u,
-                                            const TileKeys &tk, int hi, uint32_t o) {
+                                               const TileKeys &tk, int hi, uint32_t o) {
     constexpr int E = D / 32;
     const ValueRows<D, FP8> rows(p, u.seq, u.h, u.kv0);
 #pragma unroll 1
